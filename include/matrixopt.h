@@ -56,6 +56,9 @@ typedef struct CUstream_st* mo_stream_t;      /* same type as cudaStream_t */
 /* element types */
 #define MO_F32  0
 #define MO_BF16 1
+/* index types (token ids) */
+#define MO_I32  2
+#define MO_I64  3
 
 /* Newton-Schulz arithmetic */
 #define MO_NS_BF16 0   /* bf16 tensor-core operands (tcgen05), fp32 accumulate and epilogue */
@@ -272,6 +275,104 @@ int sign_vote_update_int8(const int8_t* const* signs, int M, int64_t rows, int64
  * world <= 0 or a negative size gives MO_ERR_INVALID_ARG. */
 int plan_owners(const int64_t* rows, const int64_t* cols, int n, int world, int ns_steps,
                 double w_bytes, double w_flops, int32_t* owner_out, double* load_out);
+
+/* ------------------------------------------------------------------------
+ * Operators of the training step around the optimizer: they make the
+ * gradients that muon_step_batched and the AdamW tail consume.  Matrices are
+ * row-major with a leading dimension in elements, as above; element
+ * alignment suffices unless an entry says otherwise.  All sums are float32.
+ * ------------------------------------------------------------------------ */
+
+/* Embedding lookup: out[i, :] = scale * W[ids[i], :] for i < n, W vocab x dim
+ * (float32 or bf16, ldw >= dim), out n x dim (float32 or bf16, ldo >= dim),
+ * one rounding.  ids: MO_I32 or MO_I64; an id outside [0, vocab) (padding)
+ * gives a row of zeros.  n == 0 or dim == 0 is a no-op; with vocab == 0 every
+ * row is zero.  vocab and n below 2^31 (else MO_ERR_UNSUPPORTED). */
+int embedding_lookup(const void* W, int w_dtype, int64_t vocab, int64_t dim, int64_t ldw, const void* ids,
+                     int id_dtype, int64_t n, float scale, void* out, int out_dtype, int64_t ldo,
+                     mo_stream_t stream);
+
+/* The lookup's gradient, dense: dW[v, :] = scale * sum of dY[i, :] over the
+ * i with ids[i] == v (zeros for a token that does not occur), or, with
+ * accumulate = 1, dW[v, :] += that (rows of absent tokens untouched).  The
+ * positions are sorted by token and each row is summed in float32 in a fixed
+ * order, so that the result is the same bit for bit on every call; a bf16 dW
+ * is rounded once.  Ids outside [0, vocab) contribute nothing.  A contiguous
+ * float32 dW is what mo_adamw_tail takes as g.  ws: 256-byte aligned, of
+ * embedding_grad_workspace_bytes (host only); its contents need no
+ * initialisation. */
+int embedding_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim, size_t* bytes_out);
+int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t ldy, const void* ids, int id_dtype,
+                   int64_t vocab, float scale, void* dW, int dw_dtype, int64_t ldw, int accumulate, void* ws,
+                   size_t ws_bytes, mo_stream_t stream);
+
+/* Matrix products grouped by expert.  The rows of X and dY are sorted by
+ * expert: expert e holds rows offsets[e] .. offsets[e + 1] - 1 (any number,
+ * also none); offsets is a DEVICE array of experts + 1 int32, non-decreasing,
+ * within [0, rows] (other values give wrong results, never an access out of
+ * range).  W holds one n x k matrix for each expert, expert e at
+ * W + e * stride_w (elements), ldw >= k.  bf16 operands on the tensor cores,
+ * float32 sums:
+ *   expert_linear        Y[r, :]  = X[r, :] W_e^T                  (rows x n)
+ *   expert_linear_dgrad  dX[r, :] = dY[r, :] W_e                   (rows x k)
+ *   expert_linear_wgrad  dW_e (+)= sum_r dY[r, :]^T X[r, :]        (n x k each)
+ * Rows of no expert (before offsets[0], from offsets[experts] on) give rows
+ * of zeros; an expert without rows gives dW_e = 0 (unchanged with accumulate
+ * = 1).  Outputs are float32 or bf16 (rounded once; accumulation adds before
+ * that rounding).  dW_e sits at dW + e * stride_dw: the gradient G of one
+ * mo_matrix.  Operand and output bases are 16-byte aligned and leading
+ * dimensions and strides multiples of 16 bytes (MO_ERR_ALIGNMENT), n and k
+ * any size.  rows < 2^31 - 512, n and k <= 2^20, experts <= 1024
+ * (MO_ERR_UNSUPPORTED above).  ws: 256-byte aligned, of
+ * expert_linear_workspace_bytes (host only), zero-filled once by the caller
+ * before its first use; it serves all three calls, one at a time, and
+ * mo_check_device_status reads its error word. */
+int expert_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k, int experts, size_t* bytes_out);
+int expert_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_t stride_w, const int32_t* offsets,
+                  int64_t rows, int64_t n, int64_t k, int experts, void* Y, int y_dtype, int64_t ldy, void* ws,
+                  size_t ws_bytes, mo_stream_t stream);
+int expert_linear_dgrad(const void* dY, int64_t ldy, const void* W, int64_t ldw, int64_t stride_w,
+                        const int32_t* offsets, int64_t rows, int64_t n, int64_t k, int experts, void* dX,
+                        int dx_dtype, int64_t ldx, void* ws, size_t ws_bytes, mo_stream_t stream);
+int expert_linear_wgrad(const void* dY, int64_t ldy, const void* X, int64_t ldx, const int32_t* offsets,
+                        int64_t rows, int64_t n, int64_t k, int experts, void* dW, int dw_dtype, int64_t lddw,
+                        int64_t stride_dw, int accumulate, void* ws, size_t ws_bytes, mo_stream_t stream);
+
+/* Distillation from a teacher's top logits.  For each of n rows: student
+ * logits s (vocab, float32 or bf16, ldl >= vocab) and `top` teacher entries
+ * (ids idx, logits t, each n x top, contiguous; idx int32 or int64, t float32
+ * or bf16).  An entry whose id lies outside [0, vocab) is absent.  With T =
+ * temperature > 0, p = softmax(t / T) over the present entries and q =
+ * softmax(s / T) over the vocabulary,
+ *   loss  = w T^2 sum_k p_k (log p_k - log q[idx_k])
+ *   d s_j = g w T (q_j - sum of p_k over the k with idx_k == j)
+ * where w = row_weight[row] (null: 1) and g = grad_scale.  T^2 keeps the
+ * gradient's size independent of T.  Entries with p_k = 0 (t = -inf) add
+ * nothing; q of a logit at -inf is 0 (a row of -inf only has q = 0 throughout),
+ * and p_k > 0 there makes the loss +inf.  A row with w = 0, or without a present
+ * entry above -inf, has loss 0 and gradient 0 whatever its logits hold; NaN
+ * elsewhere propagates within its row.
+ *   distill_topk_loss       writes loss[n] and stats[n][2] = {max s, sum exp((s - max)/T)}
+ *   distill_topk_grad       from the same inputs and stats writes dlogits
+ *   distill_topk_loss_grad  both in one pass over the logits
+ * dlogits is n x vocab, float32 or bf16, ldg >= vocab; it may be the logits
+ * themselves (same type and ld).  1 <= top <= 1024 (MO_ERR_UNSUPPORTED
+ * above), vocab < 2^31.  n == 0 is a no-op. */
+typedef struct {
+    int64_t n, vocab, ldl;
+    int32_t top, logits_dtype, idx_dtype, teacher_dtype;
+    float temperature, grad_scale;
+    const void*  logits;
+    const void*  idx;
+    const void*  teacher;
+    const float* row_weight;   /* n floats, or null */
+} mo_distill;
+
+int distill_topk_loss(const mo_distill* d, float* loss, float* stats, mo_stream_t stream);
+int distill_topk_grad(const mo_distill* d, const float* stats, void* dlogits, int g_dtype, int64_t ldg,
+                      mo_stream_t stream);
+int distill_topk_loss_grad(const mo_distill* d, float* loss, void* dlogits, int g_dtype, int64_t ldg,
+                           mo_stream_t stream);
 
 /* Synchronises `stream`, reads the device error word in workspace `ws`
  * (written by bounded waits inside the kernels), clears it, and returns

@@ -123,6 +123,13 @@ int mo_debug_cta_stamps(uint64_t* buf, int capacity, int max_ctas, int* recorded
 #define MO_K_VOTE     9
 #define MO_K_SPECTRAL 10  /* power-iteration spectral estimate (all of its launches) */
 #define MO_K_NS_FUSED 11  /* all NS levels of a call in one launch (Gram, polynomial, apply) */
+#define MO_K_EMBED        12  /* embedding_lookup */
+#define MO_K_EMBED_SORT   13  /* embedding_grad: positions sorted by token (all of its launches) */
+#define MO_K_EMBED_GRAD   14  /* embedding_grad: sums per token (all of its launches) */
+#define MO_K_EXPERT       15  /* expert_linear */
+#define MO_K_EXPERT_DGRAD 16  /* expert_linear_dgrad */
+#define MO_K_EXPERT_WGRAD 17  /* expert_linear_wgrad */
+#define MO_K_DISTILL      18  /* distill_topk_* */
 int mo_trace_enable(int capacity);
 int mo_trace_read(int32_t* kinds, float* ms, int cap, int* count);
 

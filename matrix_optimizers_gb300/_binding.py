@@ -19,7 +19,7 @@ c_int32, c_int64, c_float, c_double, c_void_p, c_size_t = (
 
 MO_OK, MO_ERR_INVALID_ARG, MO_ERR_ALIGNMENT, MO_ERR_WORKSPACE, MO_ERR_CUDA, MO_ERR_TIMEOUT, \
     MO_ERR_UNSUPPORTED = 0, -1, -2, -3, -4, -5, -6
-MO_F32, MO_BF16 = 0, 1
+MO_F32, MO_BF16, MO_I32, MO_I64 = 0, 1, 2, 3
 MO_NS_BF16, MO_NS_FP32 = 0, 1
 
 
@@ -59,6 +59,13 @@ class mo_ns_view(ctypes.Structure):
                 ("releases_per_tile", c_int32), ("reserved", c_int32)]
 
 
+class mo_distill(ctypes.Structure):
+    _fields_ = [("n", c_int64), ("vocab", c_int64), ("ldl", c_int64),
+                ("top", c_int32), ("logits_dtype", c_int32), ("idx_dtype", c_int32), ("teacher_dtype", c_int32),
+                ("temperature", c_float), ("grad_scale", c_float),
+                ("logits", c_void_p), ("idx", c_void_p), ("teacher", c_void_p), ("row_weight", c_void_p)]
+
+
 # (name, restype, argtypes) of every exported symbol declared in include/*.h
 _SIGNATURES = [
     ("mo_workspace_bytes", c_int32, [ctypes.POINTER(mo_matrix), c_int32, ctypes.POINTER(mo_muon_cfg),
@@ -95,6 +102,22 @@ _SIGNATURES = [
     ("plan_owners", c_int32, [ctypes.POINTER(c_int64), ctypes.POINTER(c_int64), c_int32, c_int32,
                               c_int32, c_double, c_double, ctypes.POINTER(c_int32),
                               ctypes.POINTER(c_double)]),
+    ("embedding_lookup", c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_int32, c_int64, c_float,
+                                   c_void_p, c_int32, c_int64, c_void_p]),
+    ("embedding_grad_workspace_bytes", c_int32, [c_int64, c_int64, c_int64, ctypes.POINTER(c_size_t)]),
+    ("embedding_grad", c_int32, [c_void_p, c_int32, c_int64, c_int64, c_int64, c_void_p, c_int32, c_int64, c_float,
+                                 c_void_p, c_int32, c_int64, c_int32, c_void_p, c_size_t, c_void_p]),
+    ("expert_linear_workspace_bytes", c_int32, [c_int64, c_int64, c_int64, c_int32, ctypes.POINTER(c_size_t)]),
+    ("expert_linear", c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int64,
+                                c_int32, c_void_p, c_int32, c_int64, c_void_p, c_size_t, c_void_p]),
+    ("expert_linear_dgrad", c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64,
+                                      c_int64, c_int32, c_void_p, c_int32, c_int64, c_void_p, c_size_t, c_void_p]),
+    ("expert_linear_wgrad", c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64,
+                                      c_int32, c_void_p, c_int32, c_int64, c_int64, c_int32, c_void_p, c_size_t,
+                                      c_void_p]),
+    ("distill_topk_loss", c_int32, [ctypes.POINTER(mo_distill), c_void_p, c_void_p, c_void_p]),
+    ("distill_topk_grad", c_int32, [ctypes.POINTER(mo_distill), c_void_p, c_void_p, c_int32, c_int64, c_void_p]),
+    ("distill_topk_loss_grad", c_int32, [ctypes.POINTER(mo_distill), c_void_p, c_void_p, c_int32, c_int64, c_void_p]),
     ("mo_check_device_status", c_int32, [c_void_p, c_void_p]),
     ("mo_status_string", ctypes.c_char_p, [c_int32]),
     ("mo_version", c_int32, []),
@@ -112,7 +135,8 @@ _SIGNATURES = [
 
 TRACE_KINDS = {1: "momentum_norm", 2: "norm_finalize", 3: "ns_gram", 4: "ns_poly", 5: "ns_apply",
                6: "ns_k0", 7: "adamw", 8: "sign_pack", 9: "vote_update", 10: "spectral_estimate",
-               11: "ns_fused"}
+               11: "ns_fused", 12: "embedding_lookup", 13: "embedding_sort", 14: "embedding_grad",
+               15: "expert_linear", 16: "expert_linear_dgrad", 17: "expert_linear_wgrad", 18: "distill_topk"}
 
 _lib = None
 _lock = threading.Lock()
@@ -154,6 +178,14 @@ def dtype_code(dt):
     if dt == torch.bfloat16:
         return MO_BF16
     raise MoError(MO_ERR_INVALID_ARG, f"unsupported dtype {dt}")
+
+
+def id_dtype_code(dt):
+    if dt == torch.int32:
+        return MO_I32
+    if dt == torch.int64:
+        return MO_I64
+    raise MoError(MO_ERR_INVALID_ARG, f"unsupported index dtype {dt}")
 
 
 def _ptr(t):
@@ -353,6 +385,159 @@ def plan_owners(shapes, world, ns_steps=5, w_bytes=1.0, w_flops=1.0):
     load_ = (c_double * max(1, world))() if world > 0 else None
     _check(load().plan_owners(rows, cols, n, world, ns_steps, w_bytes, w_flops, owner, load_))
     return list(owner)[:n], list(load_)[:world]
+
+
+def _need(ok, msg):
+    if not ok:
+        raise MoError(MO_ERR_INVALID_ARG, msg)
+
+
+def _on_device(*tensors):
+    """Device memory, all on one device: the library takes addresses only."""
+    dev = tensors[0].device
+    _need(all(t is None or (t.is_cuda and t.device == dev) for t in tensors), "tensors must share one CUDA device")
+
+
+def embedding_lookup(W, ids, out, scale=1.0, stream=None):
+    """out[i] = scale * W[ids[i]] for W (vocab x dim), ids (n, int32 or int64)
+    and out (n x dim); ids outside the table give zeros."""
+    _on_device(W, ids, out)
+    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be 1D and contiguous")
+    _need(out.dim() == 2 and W.dim() == 2 and out.size(0) == ids.size(0) and out.size(1) == W.size(1),
+          "out must be len(ids) x dim")
+    _check(load().embedding_lookup(_ptr(W), dtype_code(W.dtype), W.size(0), W.size(1), _ld(W), _ptr(ids),
+                                   id_dtype_code(ids.dtype), ids.size(0), scale, _ptr(out), dtype_code(out.dtype),
+                                   _ld(out), _stream(stream)))
+
+
+def embedding_grad_workspace_bytes(n, vocab, dim):
+    out = c_size_t(0)
+    _check(load().embedding_grad_workspace_bytes(n, vocab, dim, ctypes.byref(out)))
+    return out.value
+
+
+def embedding_grad(dY, ids, dW, ws, scale=1.0, accumulate=False, stream=None):
+    """dW[v] (+)= scale * sum of dY[i] over ids[i] == v, dense (vocab x dim);
+    a contiguous float32 dW is what make_tail takes as g."""
+    _on_device(dW, dY, ids, ws)
+    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be 1D and contiguous")
+    _need(dY.dim() == 2 and dW.dim() == 2 and dY.size(0) == ids.size(0) and dY.size(1) == dW.size(1),
+          "dY must be len(ids) x dim")
+    _check(load().embedding_grad(_ptr(dY), dtype_code(dY.dtype), dY.size(0), dW.size(1), _ld(dY), _ptr(ids),
+                                 id_dtype_code(ids.dtype), dW.size(0), scale, _ptr(dW), dtype_code(dW.dtype), _ld(dW),
+                                 1 if accumulate else 0, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def expert_linear_workspace_bytes(rows, n, k, experts):
+    out = c_size_t(0)
+    _check(load().expert_linear_workspace_bytes(rows, n, k, experts, ctypes.byref(out)))
+    return out.value
+
+
+def _stack(t):
+    """(ld, stride) of a stack of matrices (experts x rows x cols)."""
+    _need(t.dim() == 3 and (t.size(2) <= 1 or t.stride(2) == 1), "expert matrices must be 3D with unit column stride")
+    ld = t.stride(1) if t.size(1) > 1 else max(t.size(2), t.stride(1))
+    return ld, t.stride(0) if t.size(0) > 1 else max(t.size(1) * ld, t.stride(0))
+
+
+def _bf16(*tensors):
+    _need(all(t.dtype == torch.bfloat16 for t in tensors), "operands must be bfloat16")
+
+
+def _offsets(offsets, experts):
+    _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous() and
+          offsets.numel() == experts + 1, "offsets must be experts + 1 contiguous int32")
+    return _ptr(offsets)
+
+
+def expert_linear(X, W, offsets, Y, ws, stream=None):
+    """Y[r] = X[r] W_e^T for the rows r of expert e (offsets[e] .. offsets[e+1] - 1):
+    X rows x k and W experts x n x k in bf16, Y rows x n float32 or bf16."""
+    _on_device(X, W, offsets, Y, ws)
+    _bf16(X, W)
+    ldw, stride = _stack(W)
+    _need(X.dim() == 2 and Y.dim() == 2 and X.size(0) == Y.size(0) and X.size(1) == W.size(2) and
+          Y.size(1) == W.size(1), "X must be rows x k and Y rows x n of W's experts x n x k")
+    _check(load().expert_linear(_ptr(X), _ld(X), _ptr(W), ldw, stride, _offsets(offsets, W.size(0)), X.size(0),
+                                W.size(1), W.size(2), W.size(0), _ptr(Y), dtype_code(Y.dtype), _ld(Y), _ptr(ws),
+                                ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def expert_linear_dgrad(dY, W, offsets, dX, ws, stream=None):
+    """dX[r] = dY[r] W_e: the input's gradient of expert_linear."""
+    _on_device(dY, W, offsets, dX, ws)
+    _bf16(dY, W)
+    ldw, stride = _stack(W)
+    _need(dY.dim() == 2 and dX.dim() == 2 and dY.size(0) == dX.size(0) and dY.size(1) == W.size(1) and
+          dX.size(1) == W.size(2), "dY must be rows x n and dX rows x k of W's experts x n x k")
+    _check(load().expert_linear_dgrad(_ptr(dY), _ld(dY), _ptr(W), ldw, stride, _offsets(offsets, W.size(0)),
+                                      dY.size(0), W.size(1), W.size(2), W.size(0), _ptr(dX), dtype_code(dX.dtype),
+                                      _ld(dX), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def expert_linear_wgrad(dY, X, offsets, dW, ws, accumulate=False, stream=None):
+    """dW[e] (+)= dY_e^T X_e: the weights' gradients of expert_linear; each dW[e]
+    is the G of one make_matrix."""
+    _on_device(dY, X, offsets, dW, ws)
+    _bf16(dY, X)
+    ld, stride = _stack(dW)
+    _need(dY.dim() == 2 and X.dim() == 2 and dY.size(0) == X.size(0) and dY.size(1) == dW.size(1) and
+          X.size(1) == dW.size(2), "dY must be rows x n and X rows x k of dW's experts x n x k")
+    _check(load().expert_linear_wgrad(_ptr(dY), _ld(dY), _ptr(X), _ld(X), _offsets(offsets, dW.size(0)), X.size(0),
+                                      dW.size(1), dW.size(2), dW.size(0), _ptr(dW), dtype_code(dW.dtype), ld, stride,
+                                      1 if accumulate else 0, _ptr(ws), ws.numel() * ws.element_size(),
+                                      _stream(stream)))
+
+
+def _distill(logits, idx, teacher, temperature, row_weight, grad_scale):
+    _need(logits.dim() == 2 and idx.dim() == 2 and idx.shape == teacher.shape and idx.size(0) == logits.size(0) and
+          idx.is_contiguous() and teacher.is_contiguous(), "idx and teacher must be contiguous, rows x top")
+    if row_weight is not None:
+        _need(row_weight.dtype == torch.float32 and row_weight.is_contiguous() and
+              tuple(row_weight.shape) == (logits.size(0),), "row_weight must be contiguous float32, one per row")
+    return mo_distill(logits.size(0), logits.size(1), _ld(logits), idx.size(1), dtype_code(logits.dtype),
+                      id_dtype_code(idx.dtype), dtype_code(teacher.dtype), temperature, grad_scale,
+                      logits.data_ptr(), idx.data_ptr(), teacher.data_ptr(),
+                      None if row_weight is None else row_weight.data_ptr())
+
+
+def _f32_out(t, shape, name):
+    _need(t.dtype == torch.float32 and t.is_contiguous() and tuple(t.shape) == shape,
+          f"{name} must be contiguous float32 of shape {shape}")
+
+
+def distill_topk_loss(logits, idx, teacher, loss, stats, temperature=1.0, row_weight=None, stream=None):
+    """Per-row distillation loss from the teacher's top logits (include/matrixopt.h)
+    and the row statistics distill_topk_grad takes (rows x 2)."""
+    _on_device(logits, idx, teacher, loss, stats, row_weight)
+    d = _distill(logits, idx, teacher, temperature, row_weight, 1.0)
+    _f32_out(loss, (logits.size(0),), "loss")
+    _f32_out(stats, (logits.size(0), 2), "stats")
+    _check(load().distill_topk_loss(ctypes.byref(d), _ptr(loss), _ptr(stats), _stream(stream)))
+
+
+def distill_topk_grad(logits, idx, teacher, stats, dlogits, temperature=1.0, row_weight=None, grad_scale=1.0,
+                      stream=None):
+    """The loss's gradient by the logits, from distill_topk_loss's statistics;
+    dlogits may be the logits themselves."""
+    _on_device(logits, idx, teacher, stats, dlogits, row_weight)
+    d = _distill(logits, idx, teacher, temperature, row_weight, grad_scale)
+    _f32_out(stats, (logits.size(0), 2), "stats")
+    _need(dlogits.shape == logits.shape, "dlogits must have the logits' shape")
+    _check(load().distill_topk_grad(ctypes.byref(d), _ptr(stats), _ptr(dlogits), dtype_code(dlogits.dtype),
+                                    _ld(dlogits), _stream(stream)))
+
+
+def distill_topk_loss_grad(logits, idx, teacher, loss, dlogits, temperature=1.0, row_weight=None, grad_scale=1.0,
+                           stream=None):
+    """Loss and gradient in one pass over the logits; dlogits may be the logits."""
+    _on_device(logits, idx, teacher, loss, dlogits, row_weight)
+    d = _distill(logits, idx, teacher, temperature, row_weight, grad_scale)
+    _f32_out(loss, (logits.size(0),), "loss")
+    _need(dlogits.shape == logits.shape, "dlogits must have the logits' shape")
+    _check(load().distill_topk_loss_grad(ctypes.byref(d), _ptr(loss), _ptr(dlogits), dtype_code(dlogits.dtype),
+                                         _ld(dlogits), _stream(stream)))
 
 
 def mo_check_device_status(ws, stream=None):

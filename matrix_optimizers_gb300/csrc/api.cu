@@ -394,18 +394,28 @@ struct Stamps {
 };
 thread_local Stamps t_stamps;
 
+}  // namespace
+
+bool trace_begin(cudaStream_t s) {
+    Trace& t = t_trace;
+    return t.count >= t.capacity || cudaEventRecord(t.begin[t.count], s) == cudaSuccess;
+}
+bool trace_end(int kind, cudaStream_t s) {
+    Trace& t = t_trace;
+    if (t.count >= t.capacity) return true;
+    if (cudaEventRecord(t.end[t.count], s) != cudaSuccess) return false;
+    t.kind[t.count++] = kind;
+    return true;
+}
+
+namespace {
+
 template <typename F>
 cudaError_t traced(int kind, cudaStream_t s, F&& launch) {
-    Trace& t = t_trace;
-    const bool on = t.capacity > 0 && t.count < t.capacity;
-    if (on && cudaEventRecord(t.begin[t.count], s) != cudaSuccess) return cudaErrorUnknown;
-    cudaError_t e = launch();
-    if (on && e == cudaSuccess) {
-        if (cudaEventRecord(t.end[t.count], s) != cudaSuccess) return cudaErrorUnknown;
-        t.kind[t.count] = kind;
-        ++t.count;
-    }
-    return e;
+    if (!trace_begin(s)) return cudaErrorUnknown;
+    const cudaError_t e = launch();
+    if (e != cudaSuccess) return e;
+    return trace_end(kind, s) ? cudaSuccess : cudaErrorUnknown;
 }
 
 // A built control block (descriptor table, tensor maps, scheduled tile

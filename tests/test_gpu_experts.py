@@ -1,0 +1,224 @@
+"""Matrix products grouped by expert against the float64 oracle.
+
+Tolerances, per element: bf16 products are exact in float32 and a float32 sum
+of d terms is off by at most d 2^-23 times the sum of their magnitudes (a
+truncating accumulator loses up to one unit in the last place per addition);
+the output's rounding adds 2^-8 (bf16) or 2^-24 of the result."""
+import numpy as np
+import pytest
+import torch
+
+import matrix_optimizers_gb300 as mo
+from oracle import training as ot
+from tests.gpu_helpers import dev
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+U = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _pad8(c):
+    return (c + 7) // 8 * 8
+
+
+def _mat(rng, rows, cols, ld=None, scale=1.0):
+    ld = ld or _pad8(cols)
+    buf = torch.full((max(rows, 1), ld), float("nan"), dtype=BF16, device=dev())
+    buf[:rows, :cols] = torch.from_numpy(scale * rng.standard_normal((rows, cols))).to(BF16).to(dev())
+    return buf[:rows, :cols]
+
+
+def _stack(rng, E, rows, cols, dtype=BF16, extra=0, fill=None):
+    ld = _pad8(cols) + extra
+    buf = torch.full((E, rows + (1 if extra else 0), ld), float("nan"), dtype=dtype, device=dev())
+    v = buf[:, :rows, :cols]
+    v.copy_(torch.from_numpy(rng.standard_normal((E, rows, cols))).to(dtype) if fill is None
+            else torch.full((E, rows, cols), fill, dtype=dtype))
+    return v
+
+
+def _ws(rows, n, k, E):
+    return torch.zeros(mo.expert_linear_workspace_bytes(rows, n, k, E), dtype=torch.uint8, device=dev())
+
+
+def _offsets(sizes, first=0):
+    return np.concatenate([[first], first + np.cumsum(sizes)]).astype(np.int32)
+
+
+def _assert_close(got_t, want, mag, depth):
+    got = _f64(got_t)
+    u = U[got_t.dtype]
+    tol = (depth + 2) * 2.0 ** -23 * mag * (1 + u) + u * 1.01 * np.abs(want)
+    assert np.all(np.isfinite(got))
+    bad = np.abs(got - want) > tol
+    assert not bad.any(), (np.argwhere(bad)[:4], got[bad][:4], want[bad][:4])
+
+
+CASES = [
+    # sizes, rows before the first / after the last expert, n, k, extra columns of the leading dimensions
+    ([1], 0, 0, 1, 1, 0), ([1], 0, 0, 64, 64, 0), ([5], 0, 0, 24, 40, 0), ([0, 1, 0], 0, 0, 136, 72, 0),
+    ([3, 0, 130, 1, 17, 0], 0, 0, 200, 136, 8), ([128, 256, 64], 0, 0, 256, 128, 0),
+    ([300], 0, 0, 520, 264, 0), ([257, 255, 1, 513], 3, 5, 384, 200, 16), ([0, 0, 0], 0, 7, 72, 40, 0),
+    ([40] * 20, 0, 0, 104, 296, 0), ([33, 90], 2, 0, 77, 129, 0), ([1000, 3], 0, 0, 129, 513, 8),
+    ([0] * 70 + [9], 0, 0, 264, 64, 0)]
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("sizes,before,after,n,k,extra", CASES)
+def test_forward_and_gradients(sizes, before, after, n, k, extra, out_dtype):
+    rng = np.random.default_rng(n + k)
+    E, off = len(sizes), _offsets(sizes, before)
+    R = int(off[-1]) + after
+    X, dY = _mat(rng, R, k, _pad8(k) + extra), _mat(rng, R, n, _pad8(n) + extra)
+    W = _stack(rng, E, n, k, extra=extra)
+    o = torch.from_numpy(off).to(dev())
+    ws = _ws(R, n, k, E)
+    pad = 8
+    Y = torch.full((R, _pad8(n) + pad), 3.0, dtype=out_dtype, device=dev())
+    dX = torch.full((R, _pad8(k) + pad), 3.0, dtype=out_dtype, device=dev())
+    mo.expert_linear(X, W, o, Y[:, :n], ws)
+    mo.expert_linear_dgrad(dY, W, o, dX[:, :k], ws)
+    dW = _stack(rng, E, n, k, dtype=out_dtype, extra=extra, fill=7.0)
+    mo.expert_linear_wgrad(dY, X, o, dW, ws)
+    x, dy, w = _f64(X), _f64(dY), _f64(W)
+    _assert_close(Y[:, :n], ot.expert_linear(x, w, off), ot.expert_linear(np.abs(x), np.abs(w), off), k)
+    _assert_close(dX[:, :k], ot.expert_linear_dgrad(dy, w, off),
+                  ot.expert_linear_dgrad(np.abs(dy), np.abs(w), off), n)
+    _assert_close(dW, ot.expert_linear_wgrad(dy, x, off), ot.expert_linear_wgrad(np.abs(dy), np.abs(x), off),
+                  max(sizes))
+    assert torch.all(Y[:, n:] == 3.0) and torch.all(dX[:, k:] == 3.0)
+    out = np.ones(R, bool)
+    out[off[0]:off[-1]] = False
+    assert np.all(_f64(Y[:, :n])[out] == 0) and np.all(_f64(dX[:, :k])[out] == 0)
+    assert mo.mo_check_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("sizes", [[7, 0, 100], [600, 1]])
+def test_weight_gradient_accumulates(sizes, out_dtype):
+    rng = np.random.default_rng(4)
+    E, off, n, k = len(sizes), _offsets(sizes), 72, 136
+    R = int(off[-1])
+    X, dY = _mat(rng, R, k), _mat(rng, R, n)
+    dW = _stack(rng, E, n, k, dtype=out_dtype)
+    start = _f64(dW)
+    o, ws = torch.from_numpy(off).to(dev()), _ws(R, n, k, E)
+    mo.expert_linear_wgrad(dY, X, o, dW, ws, accumulate=True)
+    x, dy = _f64(X), _f64(dY)
+    _assert_close(dW, ot.expert_linear_wgrad(dy, x, off, start),
+                  ot.expert_linear_wgrad(np.abs(dy), np.abs(x), off, np.abs(start)), max(sizes))
+    assert np.array_equal(_f64(dW)[np.array(sizes) == 0], start[np.array(sizes) == 0])
+
+
+def test_values_of_one_expert_do_not_reach_another():
+    """Infinities and NaN in the rows (or weights) of one expert stay in its outputs,
+    also where a tile's end holds the next expert's rows."""
+    rng = np.random.default_rng(8)
+    sizes, n, k = [37, 20, 75], 136, 72
+    E, off = 3, _offsets(sizes)
+    R = int(off[-1])
+    X, dY, W = _mat(rng, R, k), _mat(rng, R, n), _stack(rng, E, n, k)
+    X[37:57] = float("nan")
+    dY[37:57] = float("inf")
+    W[1] = float("nan")
+    o, ws = torch.from_numpy(off).to(dev()), _ws(R, n, k, E)
+    Y, dX = torch.empty((R, n), dtype=BF16, device=dev()), torch.empty((R, k), dtype=BF16, device=dev())
+    dW = torch.empty((E, n, k), device=dev())
+    mo.expert_linear(X, W, o, Y, ws)
+    mo.expert_linear_dgrad(dY, W, o, dX, ws)
+    mo.expert_linear_wgrad(dY, X, o, dW, ws)
+    clean = np.r_[0:37, 57:132]
+    x, dy, w = _f64(X), _f64(dY), _f64(W)
+    x[37:57], dy[37:57], w[1] = 0, 0, 0
+    _assert_close(Y[clean], ot.expert_linear(x, w, off)[clean], ot.expert_linear(np.abs(x), np.abs(w), off)[clean], k)
+    _assert_close(dX[clean], ot.expert_linear_dgrad(dy, w, off)[clean],
+                  ot.expert_linear_dgrad(np.abs(dy), np.abs(w), off)[clean], n)
+    _assert_close(dW[[0, 2]], ot.expert_linear_wgrad(dy, x, off)[[0, 2]],
+                  ot.expert_linear_wgrad(np.abs(dy), np.abs(x), off)[[0, 2]], 75)
+    assert bool(torch.isnan(Y[37:57]).all()) and bool(torch.isnan(dW[1]).all())
+
+
+def test_results_repeat_bit_for_bit_and_on_another_stream():
+    rng = np.random.default_rng(9)
+    sizes, n, k = [700, 0, 301, 64, 1500], 392, 264
+    off = _offsets(sizes)
+    R, E = int(off[-1]), len(sizes)
+    X, dY, W = _mat(rng, R, k), _mat(rng, R, n), _stack(rng, E, n, k)
+    o, ws = torch.from_numpy(off).to(dev()), _ws(R, n, k, E)
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    runs = []
+    for _ in range(3):
+        Y, dX, dW = (torch.empty(s, device=dev()) for s in ((R, n), (R, k), (E, n, k)))
+        torch.cuda.synchronize()
+        mo.expert_linear(X, W, o, Y, ws, stream=st)
+        mo.expert_linear_dgrad(dY, W, o, dX, ws, stream=st)
+        mo.expert_linear_wgrad(dY, X, o, dW, ws, stream=st)
+        st.synchronize()
+        runs.append((Y, dX, dW))
+    assert all(torch.equal(a, b) for r in runs[1:] for a, b in zip(r, runs[0]))
+
+
+def test_offsets_outside_the_rows_stay_in_range():
+    """Wrong offsets give wrong numbers, not an access out of range (rows are held to [0, rows])."""
+    rng = np.random.default_rng(10)
+    R, n, k = 50, 72, 40
+    X, dY, W = _mat(rng, R, k), _mat(rng, R, n), _stack(rng, 3, n, k)
+    ws = _ws(R, n, k, 3)
+    Y, dX = torch.zeros((R, n), device=dev()), torch.zeros((R, k), device=dev())
+    dW = torch.zeros((3, n, k), device=dev())
+    for off in ([-5, 10, 60, 2**31 - 1], [40, 10, 30, 50], [50, 50, 50, 0]):
+        o = torch.tensor(off, dtype=torch.int32, device=dev())
+        mo.expert_linear(X, W, o, Y, ws)
+        mo.expert_linear_dgrad(dY, W, o, dX, ws)
+        mo.expert_linear_wgrad(dY, X, o, dW, ws)
+        assert mo.mo_check_device_status(ws) == 0
+
+
+def test_gradients_match_differences():
+    """The product is linear in X and in W: <Y(X + D) - Y(X - D), dY> / 2 = <dX, D>, and
+    the same for W, up to the rounding of X +- D (exact here: small integers)."""
+    rng = np.random.default_rng(11)
+    sizes, n, k = [20, 45], 48, 56
+    off = _offsets(sizes)
+    R = 65
+    ints = lambda *s: torch.from_numpy(rng.integers(-4, 5, s)).to(BF16).to(dev())
+    X, DX, W, DW, dY = ints(R, k), ints(R, k), ints(2, n, k), ints(2, n, k), ints(R, n)
+    o, ws = torch.from_numpy(off).to(dev()), _ws(R, n, k, 2)
+    Y = [torch.empty((R, n), device=dev()) for _ in range(2)]
+    dX, dW = torch.empty((R, k), device=dev()), torch.empty((2, n, k), device=dev())
+    mo.expert_linear_dgrad(dY, W, o, dX, ws)
+    mo.expert_linear_wgrad(dY, X, o, dW, ws)
+    for a, b, want in ((X + DX, W, (dX.double() * DX.double()).sum()), (X, W + DW, (dW.double() * DW.double()).sum())):
+        c, d = (X - DX, W) if b is W else (X, W - DW)
+        mo.expert_linear(a, b, o, Y[0], ws)
+        mo.expert_linear(c, d, o, Y[1], ws)
+        assert float(((Y[0].double() - Y[1].double()) * dY.double()).sum()) / 2 == float(want)   # integers below 2^24
+
+
+@pytest.mark.slow
+def test_large_sizes_against_float64_on_the_device():
+    """Long groups, many tiles: sampled rows and columns."""
+    g = torch.Generator(device=dev()).manual_seed(1)
+    sizes, n, k = [5000, 0, 1, 2047, 3001], 1544, 2056
+    off = _offsets(sizes)
+    R, E = int(off[-1]), len(sizes)
+    mk = lambda *s: torch.randn(s, generator=g, device=dev()).to(BF16)
+    X, dY, W = mk(R, k), mk(R, n), mk(E, n, k)
+    o, ws = torch.from_numpy(off).to(dev()), _ws(R, n, k, E)
+    Y, dX, dW = (torch.empty(s, device=dev()) for s in ((R, n), (R, k), (E, n, k)))
+    mo.expert_linear(X, W, o, Y, ws)
+    mo.expert_linear_dgrad(dY, W, o, dX, ws)
+    mo.expert_linear_wgrad(dY, X, o, dW, ws)
+    for e in range(E):
+        a, b = int(off[e]), int(off[e + 1])
+        x, d, w = X[a:b].double(), dY[a:b].double(), W[e].double()
+        for got, want, mag, depth in ((Y[a:b], x @ w.T, x.abs() @ w.abs().T, k), (dX[a:b], d @ w, d.abs() @ w.abs(), n),
+                                      (dW[e], d.T @ x, d.abs().T @ x.abs(), max(b - a, 1))):
+            tol = (depth + 2) * 2.0 ** -23 * mag + 2.0 ** -24 * want.abs()
+            assert bool(((got.double() - want).abs() <= tol).all())
