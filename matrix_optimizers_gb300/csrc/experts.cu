@@ -1,10 +1,31 @@
-// Matrix products grouped by expert: rows sorted by expert, expert e holding
-// rows offsets[e] .. offsets[e + 1] - 1.
+// Matrix products grouped by expert on the tensor cores: rows sorted by expert,
+// expert e holding rows offsets[e] .. offsets[e + 1] - 1 (device memory).
 //   forward  Y[r, :]  = X[r, :] W_e^T
 //   dgrad    dX[r, :] = dY[r, :] W_e
 //   wgrad    dW_e (+)= sum_r dY[r, :]^T X[r, :]
-#include <algorithm>
+//
+// One persistent CTA per SM walks tiles of D[128, N <= 256] += A B^T.  The 128
+// TMEM lanes hold output features and the columns hold tokens (forward,
+// dgrad), so that a ragged group costs N rounded up to 16 tokens and not to a
+// whole tile; the weight gradient has n on the lanes and k on the columns, and
+// its ragged sum over rows ends at a multiple of 16.
+//   forward  A = W_e   (K-major),  B = X   (K-major),  sum over k
+//   dgrad    A = W_e^T (MN-major), B = dY  (K-major),  sum over n
+//   wgrad    A = dY^T  (MN-major), B = X^T (MN-major), sum over the rows
+// Every operand comes straight from its row-major home by TMA in 128-byte
+// swizzled boxes; no transposed copy is made.
+//
+// Roles (320 threads): warps 0-7 epilogue, warp 8 TMA producer, warp 9 TMEM
+// allocation and tcgen05.mma issue into two alternating 256-column
+// accumulators.  Barrier waits are bounded (ptx.cuh); one that gives up raises
+// the CTA's abort flag, records a code in the workspace's error word and unwinds.
+#include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "ptx.cuh"
 #include "train_common.cuh"
 
 namespace mo {
@@ -15,10 +36,546 @@ namespace {
 
 enum ExpertMode { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
+constexpr int kBM = 128, kBN = 256, kBK = 64;
+constexpr int kABytes = kBM * kBK * 2;                    // 16 KB
+constexpr int kStageBytes = kABytes + kBN * kBK * 2;      // 48 KB
+constexpr int kStages = 4;
+constexpr int kEpiWarps = 8;
+constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kOutBytes = 2048;                           // one epilogue warp's store block
+constexpr int kMaxExperts = 1024;
+constexpr int kTokenGroup = 8;                            // token tiles that share a sweep over the features
+constexpr int kBoxes = 4;                                 // token boxes of 128, 64, 32 and 16 rows
+
+struct Ctl {
+    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int64_t cum[kMaxExperts + 1];                         // token tiles before expert e
+    int32_t row[kMaxExperts + 1];                         // first row of expert e, held inside [0, rows]
+};
+constexpr int kCtlBytes = (sizeof(Ctl) + 1023) / 1024 * 1024;
+constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kOutBytes + kCtlBytes + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory");
+
 struct ExpertArgs {
-    const bf16* rows_a;      // X (forward), dY (dgrad, wgrad)
+    CUtensorMap a;                 // W, or dY (wgrad)
+    CUtensorMap b[kBoxes];         // X or dY rows in boxes of 128 >> i; wgrad: b[0] is X
+    CUtensorMap o;                 // output stores
+    const int32_t* offsets;
+    void* out;
+    int64_t ldo, stride_o;
+    int32_t rows, n, k, experts;
+    int32_t out_f32, accumulate;
+    int32_t chunk;                 // K blocks summed in TMEM before the float32 sum moves on to registers
+    int* err;
+};
+
+struct Tile {
+    int e;
+    int f0;                        // first output feature on the lanes
+    int c0, cn;                    // first column (absolute token row, or k) and how many are real
+    int nmma;                      // columns of the MMA: cn rounded up to 16
+    int r0, depth;                 // wgrad: first row of the sum; length of the sum
+};
+
+// tcgen05 instruction descriptor: bf16 x bf16 -> f32, M = 128.
+__device__ __forceinline__ uint32_t instr_desc(uint32_t n, uint32_t a_mn, uint32_t b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((kBM >> 4) << 24);
+}
+
+__device__ __forceinline__ int ceil_div_i(int a, int b) { return (a + b - 1) / b; }
+
+template <int kMode>
+__device__ __forceinline__ int64_t tile_count(const ExpertArgs& p, const Ctl* ctl) {
+    if (kMode == kWgrad)
+        return static_cast<int64_t>(p.experts) * ceil_div_i(p.n, kBM) * ceil_div_i(p.k, kBN);
+    return ctl->cum[p.experts] * ceil_div_i(kMode == kFwd ? p.n : p.k, kBM);
+}
+
+// Tile u of the walk.  Forward and dgrad go expert by expert, within one in
+// groups of up to kTokenGroup token tiles, each sweeping the features with the
+// tokens innermost: the CTAs at work together then share a few thousand tokens
+// and features, which stay in L2.
+template <int kMode>
+__device__ __forceinline__ Tile tile_at(const ExpertArgs& p, const Ctl* ctl, int64_t u) {
+    Tile t;
+    if (kMode == kWgrad) {
+        const int tk = ceil_div_i(p.k, kBN), per = ceil_div_i(p.n, kBM) * tk;
+        t.e = static_cast<int>(u / per);
+        const int v = static_cast<int>(u - static_cast<int64_t>(t.e) * per);
+        t.f0 = v / tk * kBM;
+        t.c0 = v % tk * kBN;
+        t.cn = min(kBN, p.k - t.c0);
+        t.r0 = ctl->row[t.e];
+        t.depth = max(0, ctl->row[t.e + 1] - t.r0);
+    } else {
+        const int tf = ceil_div_i(kMode == kFwd ? p.n : p.k, kBM);
+        int lo = 0, hi = p.experts - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (ctl->cum[mid] * tf <= u) lo = mid; else hi = mid - 1;
+        }
+        t.e = lo;
+        const int64_t v = u - ctl->cum[lo] * tf;
+        const int nt = static_cast<int>(ctl->cum[lo + 1] - ctl->cum[lo]);
+        const int64_t per = static_cast<int64_t>(kTokenGroup) * tf;
+        const int g = static_cast<int>(v / per);
+        const int w = static_cast<int>(v - g * per);
+        const int gs = min(kTokenGroup, nt - g * kTokenGroup);
+        const int tok = g * kTokenGroup + w % gs;
+        const int m = ctl->row[lo + 1] - ctl->row[lo];
+        const int size = (ceil_div_i(m, nt) + 15) / 16 * 16;      // equal tiles, at most kBN tokens
+        t.f0 = w / gs * kBM;
+        t.c0 = ctl->row[lo] + tok * size;
+        t.cn = min(size, m - tok * size);
+        t.r0 = 0;
+        t.depth = kMode == kFwd ? p.k : p.n;
+    }
+    t.nmma = (t.cn + 15) / 16 * 16;
+    return t;
+}
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src, int32_t x, int32_t y, int32_t z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(m)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+__device__ __forceinline__ void sts_v4(uint32_t a, const uint4& v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds_v4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts_b32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts_b16(uint32_t a, bf16 v) {
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(*reinterpret_cast<unsigned short*>(&v)) : "memory");
+}
+
+// ---------------------------------------------------------------- epilogues
+// Forward and dgrad: the warp holds 32 features (lanes) x 32 tokens (v).  The
+// block goes through shared memory so that a token's features are contiguous;
+// a full block leaves by one TMA store, a block that ends inside the group by
+// plain stores of its real tokens.  A TMA store clips features past the end, but
+// in whole 16-byte pieces (measured: it wrote the elements between the end and
+// the next 16-byte boundary), so a block with an end inside a piece is stored plainly.
+template <bool kF32>
+__device__ __forceinline__ void put_tokens(const ExpertArgs& p, int cols, int f, int token, int valid, const float* v,
+                                           uint32_t buf, int lane) {
+    constexpr int kTok = kF32 ? 16 : 32;               // tokens of one 2 KB block
+    constexpr int kRow = kF32 ? 128 : 64;              // bytes of one token's 32 features
+    const bool whole = f + 32 <= cols || cols % (kF32 ? 4 : 8) == 0;
+#pragma unroll
+    for (int h = 0; h < 32 / kTok; ++h) {
+        const int nv = min(kTok, valid - h * kTok);
+        if (nv <= 0) return;                           // warp-uniform
+        if (lane == 0) bulk_wait_read_all();           // the last store has read the block
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < kTok; ++t) {
+            if (kF32)
+                sts_b32(buf + t * kRow + lane * 4, __float_as_uint(v[h * kTok + t]));
+            else
+                sts_b16(buf + t * kRow + lane * 2, __float2bfloat16_rn(v[h * kTok + t]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (nv == kTok && whole) {
+            if (lane == 0) {
+                tma_store_2d(&p.o, buf, f, token + h * kTok);
+                bulk_commit();
+            }
+        } else {
+            constexpr int kPieces = kRow / 16, kPer = kF32 ? 4 : 8;     // 16-byte pieces of a row, elements of one
+            for (int j = lane; j < nv * kPieces; j += 32) {
+                const int t = j / kPieces, q = j % kPieces, c = f + q * kPer;
+                if (c >= cols) continue;
+                const int64_t at = static_cast<int64_t>(token + h * kTok + t) * p.ldo + c;
+                const uint32_t src = buf + t * kRow + q * 16;
+                if (c + kPer <= cols) {
+                    void* dst = kF32 ? static_cast<void*>(static_cast<float*>(p.out) + at)
+                                     : static_cast<void*>(static_cast<bf16*>(p.out) + at);
+                    *reinterpret_cast<uint4*>(dst) = lds_v4(src);
+                } else {
+                    const uint4 u = lds_v4(src);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    for (int i = 0; c + i < cols; ++i) {
+                        if (kF32)
+                            static_cast<float*>(p.out)[at + i] = __uint_as_float(w[i]);
+                        else
+                            reinterpret_cast<unsigned short*>(p.out)[at + i] =
+                                static_cast<unsigned short>(w[i >> 1] >> (16 * (i & 1)));
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+}
+
+// Weight gradient: 32 rows (lanes) x 32 columns, staged with the 64-byte
+// swizzle of the store view (16-byte chunk c of row r at c ^ ((r >> 1) & 3)).
+template <bool kF32>
+__device__ __forceinline__ void put_weights(const ExpertArgs& p, int e, int row0, int col, float* v, uint32_t buf,
+                                            int lane) {
+    if (p.accumulate && row0 + lane < p.n) {
+        const int64_t at = e * p.stride_o + static_cast<int64_t>(row0 + lane) * p.ldo + col;
+        const int nv = min(32, p.k - col);
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (j < nv)
+                v[j] += kF32 ? static_cast<const float*>(p.out)[at + j]
+                             : __bfloat162float(static_cast<const bf16*>(p.out)[at + j]);
+    }
+    if (col + 32 > p.k && p.k % (kF32 ? 4 : 8) != 0) {  // ends inside a 16-byte piece (see put_tokens)
+        if (row0 + lane >= p.n) return;
+        const int64_t at = e * p.stride_o + static_cast<int64_t>(row0 + lane) * p.ldo + col;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            if (col + j >= p.k) continue;
+            if (kF32)
+                static_cast<float*>(p.out)[at + j] = v[j];
+            else
+                static_cast<bf16*>(p.out)[at + j] = __float2bfloat16_rn(v[j]);
+        }
+        return;
+    }
+    constexpr int kCols = kF32 ? 16 : 32;              // columns of one 2 KB block
+#pragma unroll
+    for (int h = 0; h < 32 / kCols; ++h) {
+        if (col + h * kCols >= p.k) return;
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            uint4 u;
+            if (kF32) {
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = v[(h * kCols + c * 4 + i) & 31];
+                u = pack16(w);
+            } else {
+                float w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = v[(c * 8 + i) & 31];
+                u = pack16(w);
+            }
+            sts_v4(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d(&p.o, buf, col + h * kCols, row0, e);
+            bulk_commit();
+        }
+    }
+}
+
+template <int kMode, bool kF32>
+__global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Ctl* ctl = reinterpret_cast<Ctl*>(smem + kStages * kStageBytes + kEpiWarps * kOutBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cols = kMode == kFwd ? p.n : p.k;        // features of the output
+
+    if (threadIdx.x == kProducerWarp * 32) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&ctl->full[s]), 1);
+            mbar_init(smem_u32(&ctl->empty[s]), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(smem_u32(&ctl->tfull[a]), 1);
+            mbar_init(smem_u32(&ctl->tempty[a]), kEpiWarps);
+        }
+        mbar_init(smem_u32(&ctl->drain), 1);
+        ctl->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+        tmem_relinquish();
+    }
+    if (warp == 0) {                                   // the experts' rows and token tiles
+        int64_t carry = 0;
+        if (lane == 0) ctl->cum[0] = 0;
+        for (int base = 0; base <= p.experts; base += 32) {
+            const int e = base + lane;
+            int a = 0, b = 0;
+            if (e <= p.experts) {
+                a = min(max(p.offsets[e], 0), p.rows);
+                ctl->row[e] = a;
+            }
+            if (e < p.experts) b = min(max(p.offsets[e + 1], 0), p.rows);
+            int64_t tiles = e < p.experts && b > a ? (b - a + kBN - 1) / kBN : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(0xffffffffu, tiles, o);
+                if (lane >= o) tiles += up;
+            }
+            if (e < p.experts) ctl->cum[e + 1] = carry + tiles;
+            carry += __shfl_sync(0xffffffffu, tiles, 31);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    volatile int* abort_flag = &ctl->abort_flag;
+    const int64_t tiles = tile_count<kMode>(p, ctl);
+
+    if (warp == kProducerWarp) {
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, narmed = 0;
+            bool ok = true;
+            for (int64_t u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
+                const Tile t = tile_at<kMode>(p, ctl, u);
+                const int nkb = ceil_div_i(t.depth, kBK);
+                const int nb = kMode == kWgrad ? (t.nmma + 63) / 64 : 0;     // 64-wide boxes of X
+                const uint32_t tx = kABytes + (kMode == kWgrad ? nb * 8192 : t.nmma * kBK * 2);
+                for (int kb = 0; kb < nkb; ++kb) {
+                    const uint32_t full = smem_u32(&ctl->full[stage]);
+                    if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err, 0x201)) {
+                        ok = false;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(full, tx);
+                    ++narmed;
+                    const uint32_t sa = smem_u32(smem + stage * kStageBytes);
+                    const uint32_t sb = sa + kABytes;
+                    const int k0 = kb * kBK;
+                    if (kMode == kFwd) {
+                        tma_load_3d(sa, &p.a, full, k0, t.f0, t.e);
+                    } else if (kMode == kDgrad) {
+                        tma_load_3d(sa, &p.a, full, t.f0, k0, t.e);
+                        tma_load_3d(sa + 8192, &p.a, full, t.f0 + 64, k0, t.e);
+                    } else {
+                        tma_load_2d(sa, &p.a, full, t.f0, t.r0 + k0);
+                        tma_load_2d(sa + 8192, &p.a, full, t.f0 + 64, t.r0 + k0);
+                        for (int i = 0; i < nb; ++i)
+                            tma_load_2d(sb + i * 8192, &p.b[0], full, t.c0 + i * 64, t.r0 + k0);
+                    }
+                    if (kMode != kWgrad) {
+                        // nmma tokens as boxes of 128, 64, 32 and 16 rows
+                        int at = 0;
+                        if (t.nmma == 256) {
+                            tma_load_2d(sb, &p.b[0], full, k0, t.c0);
+                            at = 128;
+                        }
+#pragma unroll
+                        for (int i = 0; i < kBoxes; ++i) {
+                            const int r = 128 >> i;
+                            if (t.nmma - at >= r) {
+                                tma_load_2d(sb + at * 128, &p.b[i], full, k0, t.c0 + at);
+                                at += r;
+                            }
+                        }
+                    }
+                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            // every armed copy lands before the CTA exits, also when the MMA warp gave up first
+            for (int s = 0; s < kStages; ++s) {
+                if (narmed <= static_cast<uint32_t>(s)) continue;
+                const uint32_t times = (narmed - 1u - static_cast<uint32_t>(s)) / kStages + 1u;
+                const long long t0 = clock64();
+                while (!mbar_try_wait(smem_u32(&ctl->full[s]), (times - 1u) & 1u) && clock64() - t0 < kWaitCycles) {}
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        int q = 0;                                      // chunks so far: accumulator ping-pong
+        for (int64_t u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
+            const Tile t = tile_at<kMode>(p, ctl, u);
+            const int nkb = ceil_div_i(t.depth, kBK);
+            const uint32_t idesc = instr_desc(t.nmma, kMode != kFwd, kMode == kWgrad);
+            // K-major operands: 8-row groups 1 KB apart, 32 bytes per 16-wide step.
+            // MN-major operands: 64-column blocks 8 KB apart, 8-row K groups 1 KB
+            // apart, two of them (2 KB) per step.
+            const uint64_t ad0 = kMode == kFwd ? sdesc_sw128(0, 16, 1024) : sdesc_sw128(0, 8192, 1024);
+            const uint64_t bd0 = kMode == kWgrad ? sdesc_sw128(0, 8192, 1024) : sdesc_sw128(0, 16, 1024);
+            constexpr uint32_t a_step = (kMode == kFwd ? 32 : 2048) >> 4, b_step = (kMode == kWgrad ? 2048 : 32) >> 4;
+            int in_chunk = 0;
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (in_chunk == 0) {
+                    bool free_ = true;
+                    if (lane == 0)
+                        free_ = mbar_wait_bounded(smem_u32(&ctl->tempty[q & 1]), ((q >> 1) & 1) ^ 1u, abort_flag, p.err, 0x202);
+                    if (!__shfl_sync(0xffffffffu, free_, 0)) { ok = false; break; }
+                    tc_fence_after();
+                }
+                bool there = true;
+                if (lane == 0)
+                    there = mbar_wait_bounded(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err, 0x203);
+                if (!__shfl_sync(0xffffffffu, there, 0)) { ok = false; break; }
+                const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+                int steps = kBK / 16;
+                if (kMode == kWgrad && kb + 1 == nkb) {
+                    // the sum ends inside this block: the rows up to the next multiple of
+                    // 16 belong to another expert (or to none) and become zero in both
+                    // operands, so that not even their infinities or NaN reach the sum
+                    const int v = t.depth - kb * kBK, end = (v + 15) / 16 * 16;
+                    steps = end / 16;
+                    if (v != end) {
+                        __syncwarp();                   // the copies landed (seen by lane 0)
+                        const int boxes = 2 + (t.nmma + 63) / 64, per = (end - v) * 8;
+                        for (int i = lane; i < boxes * per; i += 32)
+                            sts_v4(sa + (i / per) * 8192 + v * 128 + (i % per) * 16, make_uint4(0, 0, 0, 0));
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                if (lane == 0) {
+                    tc_fence_after();
+                    const uint32_t d = tmem + static_cast<uint32_t>((q & 1) * kBN);
+                    for (int k = 0; k < steps; ++k)
+                        umma_bf16(d, ad0 + ((sa >> 4) + k * a_step), bd0 + ((sb >> 4) + k * b_step), idesc,
+                                  (in_chunk | k) != 0 ? 1u : 0u);
+                    umma_commit(smem_u32(&ctl->empty[stage]));
+                }
+                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                if (++in_chunk == p.chunk || kb + 1 == nkb) {
+                    if (lane == 0) umma_commit(smem_u32(&ctl->tfull[q & 1]));
+                    ++q;
+                    in_chunk = 0;
+                }
+                __syncwarp();
+            }
+        }
+        if (lane == 0) {                                // all issued MMAs complete before TMEM is released
+            umma_commit(smem_u32(&ctl->drain));
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < kWaitCycles) {}
+        }
+    } else {
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t buf = smem_u32(smem + kStages * kStageBytes + warp * kOutBytes);
+        if (kMode != kWgrad) {                          // rows of no expert
+            const int head = ctl->row[0], tail = ctl->row[p.experts];
+            const int64_t extra = static_cast<int64_t>(head) + (p.rows - tail);
+            for (int64_t r = blockIdx.x * kEpiWarps + warp; r < extra; r += static_cast<int64_t>(gridDim.x) * kEpiWarps) {
+                const int64_t at = (r < head ? r : tail + (r - head)) * p.ldo;
+                for (int c = lane; c < cols; c += 32) {
+                    if (kF32)
+                        static_cast<float*>(p.out)[at + c] = 0.f;
+                    else
+                        static_cast<bf16*>(p.out)[at + c] = __float2bfloat16_rn(0.f);
+                }
+            }
+        }
+        bool ok = true;
+        int q = 0;
+        for (int64_t u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
+            const Tile t = tile_at<kMode>(p, ctl, u);
+            const int nkb = ceil_div_i(t.depth, kBK), chunks = ceil_div_i(nkb, p.chunk);
+            float v[4][32];                             // this lane's row of the warp's 32-column groups
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[g][j] = 0.f;
+            for (int c = 0; c < chunks; ++c, ++q) {
+                ok = mbar_wait_bounded(smem_u32(&ctl->tfull[q & 1]), (q >> 1) & 1, abort_flag, p.err, 0x204);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int col = (2 * g + half) * 32;
+                    if (col >= t.nmma) continue;        // warp-uniform
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                           static_cast<uint32_t>((q & 1) * kBN + col), r);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[g][j] += __uint_as_float(r[j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[q & 1]));
+            }
+            if (!ok) break;
+            if (kMode == kWgrad && t.depth == 0 && p.accumulate) continue;
+            const int f = t.f0 + quarter * 32;
+            if (f >= (kMode == kWgrad ? p.n : cols)) continue;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int col = (2 * g + half) * 32;
+                if (col >= t.cn) continue;
+                if (kMode == kWgrad)
+                    put_weights<kF32>(p, t.e, f, t.c0 + col, v[g], buf, lane);
+                else
+                    put_tokens<kF32>(p, cols, f, t.c0 + col, min(32, t.cn - col), v[g], buf, lane);
+            }
+        }
+        if (lane == 0) bulk_wait_all();                 // no store still reads this CTA's shared memory
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Zeros for outputs that no sum reaches (k == 0 or n == 0 in a product, no rows at all in a weight gradient).
+__global__ void __launch_bounds__(256) fill_zero_kernel(void* out, int out_f32, int64_t rows, int64_t cols, int64_t ld,
+                                                        int64_t stride, int64_t total) {
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
+        const int64_t r = i / cols, e = r / rows;
+        const int64_t at = e * stride + (r - e * rows) * ld + (i - r * cols);
+        if (out_f32)
+            static_cast<float*>(out)[at] = 0.f;
+        else
+            static_cast<bf16*>(out)[at] = __float2bfloat16_rn(0.f);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+bool get_encode() {
+    std::call_once(g_encode_once, [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    return g_encode != nullptr;
+}
+
+// `depth` matrices of rows x cols (one: a 2D view): boxes of box_rows x box_cols.
+bool encode(CUtensorMap* map, const void* base, int dt, int64_t cols, int64_t rows, int64_t depth, int64_t ld,
+            int64_t stride, int rank, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+    const size_t sz = op_elem_size(dt);
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(depth)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * sz), static_cast<cuuint64_t>((depth > 1 ? stride : ld) * sz)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    return g_encode(map, dt == MO_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                    static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, step,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// What a call works on, before tensor maps.
+struct Request {
+    const void* a;                 // rows operand: X (forward), dY (dgrad, wgrad)
     int64_t lda;
-    const bf16* b;           // W, or X (wgrad)
+    const void* b;                 // W, or X (wgrad)
     int64_t ldb, stride_b;
     void* out;
     int64_t ldo, stride_o;
@@ -27,94 +584,30 @@ struct ExpertArgs {
     int experts, out_dtype, accumulate;
 };
 
-// First row of expert e, held inside [0, rows] whatever the caller's array says.
-__device__ __forceinline__ int64_t row_begin(const ExpertArgs& a, int e) {
-    const int64_t o = a.offsets[e];
-    return o < 0 ? 0 : o > a.rows ? a.rows : o;
+template <int kMode, bool kF32>
+cudaError_t launch_expert(const ExpertArgs& p, int64_t most_tiles, cudaStream_t s) {
+    static std::atomic<uint64_t> attr_set{0};           // one bit per device ordinal
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(attr_set.load() & bit)) {
+        e = cudaFuncSetAttribute(expert_kernel<kMode, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+        if (e != cudaSuccess) return e;
+        attr_set.fetch_or(bit);
+    }
+    const int grid = static_cast<int>(std::min<int64_t>(most_tiles, device_sm_count()));
+    expert_kernel<kMode, kF32><<<grid, kThreads, kSmemBytes, s>>>(p);
+    return cudaGetLastError();
 }
 
-constexpr int kT = 64, kTK = 16;
-
-// 64 x 64 tile of out[i, j] = sum_k A(i, k) B(j, k).
-template <typename FA, typename FB>
-__device__ __forceinline__ void tile_product(FA&& fa, FB&& fb, int64_t depth, float (&acc)[4][4]) {
-    __shared__ float sa[kTK][kT + 1], sb[kTK][kT + 1];
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    for (int64_t k0 = 0; k0 < depth; k0 += kTK) {
-        for (int q = threadIdx.x; q < kT * kTK; q += 256) {
-            const int i = q / kTK, k = q % kTK;
-            sa[k][i] = k0 + k < depth ? fa(i, k0 + k) : 0.f;
-            sb[k][i] = k0 + k < depth ? fb(i, k0 + k) : 0.f;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kTK; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][ty * 4 + i], sb[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
-}
-
-__device__ __forceinline__ void put(const ExpertArgs& a, int64_t at, float v) {
-    if (a.out_dtype == MO_F32) {
-        float* p = static_cast<float*>(a.out) + at;
-        *p = a.accumulate ? *p + v : v;
-    } else {
-        bf16* p = static_cast<bf16*>(a.out) + at;
-        *p = __float2bfloat16_rn(a.accumulate ? __bfloat162float(*p) + v : v);
-    }
-}
-
-template <int kMode>
-__global__ void __launch_bounds__(256) expert_kernel(const __grid_constant__ ExpertArgs a) {
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    const int64_t cols = kMode == kFwd ? a.n : a.k, col0 = static_cast<int64_t>(blockIdx.x) * kT;
-    if (kMode == kWgrad) {
-        const int64_t i0 = static_cast<int64_t>(blockIdx.y) * kT;
-        for (int e = blockIdx.z; e < a.experts; e += gridDim.z) {
-            const int64_t r0 = row_begin(a, e), r1 = row_begin(a, e + 1);
-            float acc[4][4] = {};
-            tile_product([&](int i, int64_t r) { return i0 + i < a.n ? __bfloat162float(a.rows_a[(r0 + r) * a.lda + i0 + i]) : 0.f; },
-                         [&](int j, int64_t r) { return col0 + j < a.k ? __bfloat162float(a.b[(r0 + r) * a.ldb + col0 + j]) : 0.f; },
-                         r1 > r0 ? r1 - r0 : 0, acc);
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t n = i0 + ty * 4 + i, k = col0 + tx * 4 + j;
-                    if (n < a.n && k < a.k) put(a, e * a.stride_o + n * a.ldo + k, acc[i][j]);
-                }
-        }
-        return;
-    }
-    // row tiles of every expert in turn; e == -1 / experts: the rows of none
-    int64_t t = 0;
-    for (int e = -1; e <= a.experts; ++e) {
-        const int64_t r0 = e < 0 ? 0 : row_begin(a, e);
-        const int64_t r1 = e == a.experts ? a.rows : row_begin(a, e + 1);
-        for (int64_t i0 = r0; i0 < r1; i0 += kT, ++t) {
-            if (t % gridDim.y != blockIdx.y) continue;
-            float acc[4][4] = {};
-            const int64_t depth = e < 0 || e == a.experts ? 0 : kMode == kFwd ? a.k : a.n;
-            const bf16* w = a.b + e * a.stride_b;
-            tile_product([&](int i, int64_t k) { return i0 + i < r1 ? __bfloat162float(a.rows_a[(i0 + i) * a.lda + k]) : 0.f; },
-                         [&](int j, int64_t k) {
-                             if (col0 + j >= cols) return 0.f;
-                             return __bfloat162float(kMode == kFwd ? w[(col0 + j) * a.ldb + k] : w[k * a.ldb + col0 + j]);
-                         },
-                         depth, acc);
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) {
-                    const int64_t r = i0 + ty * 4 + i, c = col0 + tx * 4 + j;
-                    if (r < r1 && c < cols) put(a, r * a.ldo + c, acc[i][j]);
-                }
-        }
-    }
-}
+// A float32 result's sums leave TMEM every kF32Chunk K blocks: the tensor core's
+// accumulator drops bits below its last place, always towards zero, and adding
+// the pieces in registers (to nearest) keeps that drift from growing with the sum.
+constexpr int kF32Chunk = 8;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
 constexpr int64_t kMaxSide = int64_t(1) << 20;
-constexpr int kMaxExperts = 1024;
 constexpr size_t kExpertHeader = 256;      // the error word that mo_check_device_status reads
 
 size_t expert_ws_bytes() { return kExpertHeader; }
@@ -138,26 +631,62 @@ int check_stack(int dt, int64_t rows, int64_t ld, int64_t stride, int experts) {
     return MO_OK;
 }
 
-int run_expert(int mode, const ExpertArgs& a, void* ws, size_t ws_bytes, mo_stream_t stream) {
-    if (a.offsets == nullptr) return MO_ERR_INVALID_ARG;
-    if (!op_aligned(a.offsets, 4)) return MO_ERR_ALIGNMENT;
+int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_t stream) {
+    if (q.offsets == nullptr) return MO_ERR_INVALID_ARG;
+    if (!op_aligned(q.offsets, 4)) return MO_ERR_ALIGNMENT;
     const int st = op_check_ws(ws, ws_bytes, expert_ws_bytes());
     if (st != MO_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool f32 = q.out_dtype == MO_F32;
+    const int64_t cols = mode == kFwd ? q.n : q.k;      // of the output
+    const int64_t depth = mode == kFwd ? q.k : mode == kDgrad ? q.n : q.rows;
+    if (depth == 0) {
+        if (q.accumulate) return MO_OK;
+        const int64_t rows = mode == kWgrad ? q.n : q.rows, total = rows * cols * (mode == kWgrad ? q.experts : 1);
+        return op_status(op_traced(MO_K_EXPERT + mode, s, [&] {
+            fill_zero_kernel<<<static_cast<unsigned>(std::min<int64_t>(op_ceil_div(total, 256), 16384)), 256, 0, s>>>(
+                q.out, f32, rows, cols, q.ldo, q.stride_o, total);
+            return cudaGetLastError();
+        }));
+    }
+    if (!get_encode()) return MO_ERR_CUDA;
+    ExpertArgs p;
+    bool ok;
+    int64_t most_tiles;
+    constexpr auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (mode == kWgrad) {
+        ok = encode(&p.a, q.a, MO_BF16, q.n, q.rows, 1, q.lda, 0, 2, 64, 64, k128) &&
+             encode(&p.b[0], q.b, MO_BF16, q.k, q.rows, 1, q.ldb, 0, 2, 64, 64, k128) &&
+             encode(&p.o, q.out, q.out_dtype, q.k, q.n, q.experts, q.ldo, q.stride_o, 3, f32 ? 16 : 32, 32,
+                    CU_TENSOR_MAP_SWIZZLE_64B);
+        for (int i = 1; i < kBoxes; ++i) p.b[i] = p.b[0];
+        most_tiles = q.experts * op_ceil_div(q.n, kBM) * op_ceil_div(q.k, kBN);
+    } else {
+        ok = encode(&p.a, q.b, MO_BF16, q.k, q.n, q.experts, q.ldb, q.stride_b, 3, 64, mode == kFwd ? 128 : 64, k128) &&
+             encode(&p.o, q.out, q.out_dtype, cols, q.rows, 1, q.ldo, 0, 2, 32, f32 ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_NONE);
+        for (int i = 0; i < kBoxes; ++i)
+            ok = ok && encode(&p.b[i], q.a, MO_BF16, depth, q.rows, 1, q.lda, 0, 2, 64, 128 >> i, k128);
+        // each expert may end in a tile of its own
+        most_tiles = (q.rows / kBN + std::min<int64_t>(q.experts, q.rows)) * op_ceil_div(cols, kBM);
+    }
+    if (!ok) return MO_ERR_UNSUPPORTED;                 // a stride past what a tensor map holds (2^40 bytes)
+    p.offsets = q.offsets;
+    p.out = q.out;
+    p.ldo = q.ldo;
+    p.stride_o = q.stride_o;
+    p.rows = static_cast<int32_t>(q.rows);
+    p.n = static_cast<int32_t>(q.n);
+    p.k = static_cast<int32_t>(q.k);
+    p.experts = q.experts;
+    p.out_f32 = f32;
+    p.accumulate = q.accumulate;
+    p.chunk = f32 ? kF32Chunk : 1 << 26;                 // more blocks than any sum has
+    p.err = static_cast<int*>(ws);
     return op_status(op_traced(MO_K_EXPERT + mode, s, [&] {
-        const unsigned gx = static_cast<unsigned>(op_ceil_div(mode == kFwd ? a.n : a.k, kT));
-        if (mode == kWgrad) {
-            const dim3 grid(gx, static_cast<unsigned>(op_ceil_div(a.n, kT)), static_cast<unsigned>(a.experts));
-            expert_kernel<kWgrad><<<grid, 256, 0, s>>>(a);
-        } else {
-            const int64_t tiles = op_ceil_div(a.rows, kT) + a.experts + 2;
-            const dim3 grid(gx, static_cast<unsigned>(std::min<int64_t>(tiles, 4096)));
-            if (mode == kFwd)
-                expert_kernel<kFwd><<<grid, 256, 0, s>>>(a);
-            else
-                expert_kernel<kDgrad><<<grid, 256, 0, s>>>(a);
-        }
-        return cudaGetLastError();
+        if (mode == kFwd) return f32 ? launch_expert<kFwd, true>(p, most_tiles, s) : launch_expert<kFwd, false>(p, most_tiles, s);
+        if (mode == kDgrad)
+            return f32 ? launch_expert<kDgrad, true>(p, most_tiles, s) : launch_expert<kDgrad, false>(p, most_tiles, s);
+        return f32 ? launch_expert<kWgrad, true>(p, most_tiles, s) : launch_expert<kWgrad, false>(p, most_tiles, s);
     }));
 }
 
@@ -186,7 +715,7 @@ int expert_linear(const void* X, int64_t ldx, const void* W, int64_t ldw, int64_
     if ((st = check_matrix(W, MO_BF16, k, ldw, k > 0)) != MO_OK) return st;
     if ((st = check_stack(MO_BF16, n, ldw, stride_w, experts)) != MO_OK) return st;
     if ((st = check_matrix(Y, y_dtype, n, ldy, true)) != MO_OK) return st;
-    const ExpertArgs a = {static_cast<const bf16*>(X), ldx, static_cast<const bf16*>(W), ldw, stride_w, Y, ldy, 0,
+    const Request a = {X, ldx, W, ldw, stride_w, Y, ldy, 0,
                           offsets, rows, n, k, experts, y_dtype, 0};
     return run_expert(kFwd, a, ws, ws_bytes, stream);
 }
@@ -202,7 +731,7 @@ int expert_linear_dgrad(const void* dY, int64_t ldy, const void* W, int64_t ldw,
     if ((st = check_matrix(W, MO_BF16, k, ldw, n > 0)) != MO_OK) return st;
     if ((st = check_stack(MO_BF16, n, ldw, stride_w, experts)) != MO_OK) return st;
     if ((st = check_matrix(dX, dx_dtype, k, ldx, true)) != MO_OK) return st;
-    const ExpertArgs a = {static_cast<const bf16*>(dY), ldy, static_cast<const bf16*>(W), ldw, stride_w, dX, ldx, 0,
+    const Request a = {dY, ldy, W, ldw, stride_w, dX, ldx, 0,
                           offsets, rows, n, k, experts, dx_dtype, 0};
     return run_expert(kDgrad, a, ws, ws_bytes, stream);
 }
@@ -218,7 +747,7 @@ int expert_linear_wgrad(const void* dY, int64_t ldy, const void* X, int64_t ldx,
     if ((st = check_matrix(X, MO_BF16, k, ldx, rows > 0)) != MO_OK) return st;
     if ((st = check_matrix(dW, dw_dtype, k, lddw, true)) != MO_OK) return st;
     if ((st = check_stack(dw_dtype, n, lddw, stride_dw, experts)) != MO_OK) return st;
-    const ExpertArgs a = {static_cast<const bf16*>(dY), ldy, static_cast<const bf16*>(X), ldx, 0, dW, lddw, stride_dw,
+    const Request a = {dY, ldy, X, ldx, 0, dW, lddw, stride_dw,
                           offsets, rows, n, k, experts, dw_dtype, accumulate};
     return run_expert(kWgrad, a, ws, ws_bytes, stream);
 }
