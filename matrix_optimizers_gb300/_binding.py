@@ -127,6 +127,7 @@ _SIGNATURES = [
     ("mo_debug_set_ns_fused", c_int32, [c_int32]),
     ("mo_debug_inject_dep_stall", c_int32, [c_int32, c_int64]),
     ("mo_debug_set_ns_pair", c_int32, [c_int32]),
+    ("mo_debug_set_expert_pair", c_int32, [c_int32]),
     ("mo_debug_cta_stamps", c_int32, [c_void_p, c_int32, c_int32, ctypes.POINTER(c_int32)]),
     ("mo_trace_enable", c_int32, [c_int32]),
     ("mo_trace_read", c_int32, [ctypes.POINTER(c_int32), ctypes.POINTER(c_float), c_int32,
@@ -575,6 +576,14 @@ def mo_debug_set_ns_fused(on):
     prev = load().mo_debug_set_ns_fused(int(on))
     _check(prev if prev < 0 else 0)
     return prev
+
+
+def mo_debug_set_expert_pair(on):
+    """Tile geometry of the expert products: 0 single CTAs, 1 CTA pairs, -1
+    (default) by the sizes; returns the previous setting."""
+    prev = load().mo_debug_set_expert_pair(int(on))
+    _check(prev if prev < 0 else 0)
+    return prev - 1
 
 
 def mo_debug_cta_stamps(buf, capacity, max_ctas):

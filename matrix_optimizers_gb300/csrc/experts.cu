@@ -36,10 +36,23 @@ namespace {
 
 enum ExpertMode { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
-constexpr int kBM = 128, kBN = 256, kBK = 64;
+constexpr int kBM = 128, kBN = 256, kBK = 64;             // lanes, columns and depth of one CTA's tile and stage
 constexpr int kABytes = kBM * kBK * 2;                    // 16 KB
-constexpr int kStageBytes = kABytes + kBN * kBK * 2;      // 48 KB
-constexpr int kStages = 4;
+constexpr int kRingBytes = 196608;
+constexpr int kMaxStages = 6;
+// Single CTA (cta_group::1): a stage holds 128 features and up to 256 columns
+// (48 KB, four stages).  CTA pair (cta_group::2): 256 features x up to 256
+// columns per pair, each CTA holding its 128 features and half the columns
+// (32 KB, six stages), its own 128 x 256 accumulator and its own epilogue.
+template <bool kPair>
+struct Geo {
+    static constexpr int kCtas = kPair ? 2 : 1;
+    static constexpr int kStageBytes = kABytes + kBN / kCtas * kBK * 2;
+    static constexpr int kStages = kRingBytes / kStageBytes;
+    static constexpr int kFeatures = kCtas * kBM;
+    static constexpr int kRound = kPair ? 32 : 16;        // columns of an MMA come in multiples of
+};
+static_assert(Geo<true>::kStages <= kMaxStages && Geo<false>::kStages <= kMaxStages, "ring depth");
 constexpr int kEpiWarps = 8;
 constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kThreads = 32 * (kEpiWarps + 2);
@@ -49,14 +62,15 @@ constexpr int kTokenGroup = 8;                            // token tiles that sh
 constexpr int kBoxes = 4;                                 // token boxes of 128, 64, 32 and 16 rows
 
 struct Ctl {
-    uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
+    uint64_t full[kMaxStages], empty[kMaxStages], tfull[2], tempty[2], drain;
+    uint64_t tail[kMaxStages], tail_peer[kMaxStages];     // pair, wgrad: a sum's ragged last block in that stage
     uint32_t tmem_base;
     int abort_flag;
     int64_t cum[kMaxExperts + 1];                         // token tiles before expert e
     int32_t row[kMaxExperts + 1];                         // first row of expert e, held inside [0, rows]
 };
 constexpr int kCtlBytes = (sizeof(Ctl) + 1023) / 1024 * 1024;
-constexpr int kSmemBytes = kStages * kStageBytes + kEpiWarps * kOutBytes + kCtlBytes + 1024;
+constexpr int kSmemBytes = kRingBytes + kEpiWarps * kOutBytes + kCtlBytes + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory");
 
 struct ExpertArgs {
@@ -74,44 +88,45 @@ struct ExpertArgs {
 
 struct Tile {
     int e;
-    int f0;                        // first output feature on the lanes
+    int f0;                        // first output feature on the lanes (of the pair's first CTA)
     int c0, cn;                    // first column (absolute token row, or k) and how many are real
-    int nmma;                      // columns of the MMA: cn rounded up to 16
+    int nmma;                      // columns of the MMA: cn rounded up to 16 (pair: 32)
     int r0, depth;                 // wgrad: first row of the sum; length of the sum
 };
 
-// tcgen05 instruction descriptor: bf16 x bf16 -> f32, M = 128.
-__device__ __forceinline__ uint32_t instr_desc(uint32_t n, uint32_t a_mn, uint32_t b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((kBM >> 4) << 24);
+// tcgen05 instruction descriptor: bf16 x bf16 -> f32, M x N.
+__device__ __forceinline__ uint32_t instr_desc(uint32_t m, uint32_t n, uint32_t a_mn, uint32_t b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
 __device__ __forceinline__ int ceil_div_i(int a, int b) { return (a + b - 1) / b; }
 
-template <int kMode>
+template <int kMode, bool kPair>
 __device__ __forceinline__ int64_t tile_count(const ExpertArgs& p, const Ctl* ctl) {
     if (kMode == kWgrad)
-        return static_cast<int64_t>(p.experts) * ceil_div_i(p.n, kBM) * ceil_div_i(p.k, kBN);
-    return ctl->cum[p.experts] * ceil_div_i(kMode == kFwd ? p.n : p.k, kBM);
+        return static_cast<int64_t>(p.experts) * ceil_div_i(p.n, Geo<kPair>::kFeatures) * ceil_div_i(p.k, kBN);
+    return ctl->cum[p.experts] * ceil_div_i(kMode == kFwd ? p.n : p.k, Geo<kPair>::kFeatures);
 }
 
 // Tile u of the walk.  Forward and dgrad go expert by expert, within one in
 // groups of up to kTokenGroup token tiles, each sweeping the features with the
 // tokens innermost: the CTAs at work together then share a few thousand tokens
 // and features, which stay in L2.
-template <int kMode>
+template <int kMode, bool kPair>
 __device__ __forceinline__ Tile tile_at(const ExpertArgs& p, const Ctl* ctl, int64_t u) {
+    using G = Geo<kPair>;
     Tile t;
     if (kMode == kWgrad) {
-        const int tk = ceil_div_i(p.k, kBN), per = ceil_div_i(p.n, kBM) * tk;
+        const int tk = ceil_div_i(p.k, kBN), per = ceil_div_i(p.n, G::kFeatures) * tk;
         t.e = static_cast<int>(u / per);
         const int v = static_cast<int>(u - static_cast<int64_t>(t.e) * per);
-        t.f0 = v / tk * kBM;
+        t.f0 = v / tk * G::kFeatures;
         t.c0 = v % tk * kBN;
         t.cn = min(kBN, p.k - t.c0);
         t.r0 = ctl->row[t.e];
         t.depth = max(0, ctl->row[t.e + 1] - t.r0);
     } else {
-        const int tf = ceil_div_i(kMode == kFwd ? p.n : p.k, kBM);
+        const int tf = ceil_div_i(kMode == kFwd ? p.n : p.k, G::kFeatures);
         int lo = 0, hi = p.experts - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -127,13 +142,13 @@ __device__ __forceinline__ Tile tile_at(const ExpertArgs& p, const Ctl* ctl, int
         const int tok = g * kTokenGroup + w % gs;
         const int m = ctl->row[lo + 1] - ctl->row[lo];
         const int size = (ceil_div_i(m, nt) + 15) / 16 * 16;      // equal tiles, at most kBN tokens
-        t.f0 = w / gs * kBM;
+        t.f0 = w / gs * G::kFeatures;
         t.c0 = ctl->row[lo] + tok * size;
         t.cn = min(size, m - tok * size);
         t.r0 = 0;
         t.depth = kMode == kFwd ? p.k : p.n;
     }
-    t.nmma = (t.cn + 15) / 16 * 16;
+    t.nmma = (t.cn + G::kRound - 1) / G::kRound * G::kRound;
     return t;
 }
 
@@ -157,6 +172,73 @@ __device__ __forceinline__ void sts_b32(uint32_t a, uint32_t v) {
 }
 __device__ __forceinline__ void sts_b16(uint32_t a, bf16 v) {
     asm volatile("st.shared.b16 [%0], %1;" ::"r"(a), "h"(*reinterpret_cast<unsigned short*>(&v)) : "memory");
+}
+
+// A wait that also acquires what the arriving CTA of the cluster wrote.
+__device__ __forceinline__ bool mbar_wait_cluster_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err,
+                                                          int code) {
+    const long long t0 = clock64();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitCycles) {
+            *abort_flag = 1;
+            atomicCAS(err, 0, code);
+            return false;
+        }
+    }
+}
+
+// A bounded wait by a whole warp; the vote tells the compiler that the outcome
+// (and so the control flow and the addresses derived from it) is the same in all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err, int code) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, err, code));
+}
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
+// One operand box, the pair form counting on an mbarrier of either CTA.
+template <bool kPair>
+__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
+    if constexpr (kPair)
+        tma_load_2d_pair(dst, m, bar, x, y);
+    else
+        tma_load_2d(dst, m, bar, x, y);
+}
+template <bool kPair>
+__device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y, int z) {
+    if constexpr (kPair)
+        tma_load_3d_pair(dst, m, bar, x, y, z);
+    else
+        tma_load_3d(dst, m, bar, x, y, z);
+}
+
+// The rows from `v` up to the next multiple of 16 of a weight gradient's last
+// block belong to another expert (or to none): they become zero in both
+// operands, so that not even their infinities or NaN reach the sum.  Called by a
+// whole warp after the block's copies landed.
+__device__ __forceinline__ void zero_tail(uint32_t stage, int boxes, int v, int lane) {
+    const int per = ((v + 15) / 16 * 16 - v) * 8;         // 16-byte pieces per 64-wide box
+    for (int i = lane; i < boxes * per; i += 32)
+        sts_v4(stage + (i / per) * 8192 + v * 128 + (i % per) * 16, make_uint4(0, 0, 0, 0));
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- epilogues
@@ -278,30 +360,52 @@ __device__ __forceinline__ void put_weights(const ExpertArgs& p, int e, int row0
     }
 }
 
-template <int kMode, bool kF32>
+// Arrives on `bar` (in both CTAs of a pair) when the MMAs issued so far are done.
+template <bool kPair>
+__device__ __forceinline__ void commit(uint32_t bar) {
+    if constexpr (kPair)
+        umma_commit_pair(bar, 0x3);
+    else
+        umma_commit(bar);
+}
+
+template <int kMode, bool kF32, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs p) {
+    using G = Geo<kPair>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    Ctl* ctl = reinterpret_cast<Ctl*>(smem + kStages * kStageBytes + kEpiWarps * kOutBytes);
+    Ctl* ctl = reinterpret_cast<Ctl*>(smem + kRingBytes + kEpiWarps * kOutBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int cols = kMode == kFwd ? p.n : p.k;        // features of the output
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;   // rank 0 leads the pair
+    const bool leader = rank == 0;
+    const int unit = static_cast<int>(blockIdx.x) / G::kCtas, units = static_cast<int>(gridDim.x) / G::kCtas;
 
     if (threadIdx.x == kProducerWarp * 32) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < G::kStages; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), 1);
             mbar_init(smem_u32(&ctl->empty[s]), 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(smem_u32(&ctl->tfull[a]), 1);
-            mbar_init(smem_u32(&ctl->tempty[a]), kEpiWarps);
+            mbar_init(smem_u32(&ctl->tempty[a]), G::kCtas * kEpiWarps);
+        }
+        for (int s = 0; s < G::kStages; ++s) {
+            mbar_init(smem_u32(&ctl->tail[s]), 1);
+            mbar_init(smem_u32(&ctl->tail_peer[s]), 1);
         }
         mbar_init(smem_u32(&ctl->drain), 1);
         ctl->abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(smem_u32(&ctl->tmem_base), 512);
-        tmem_relinquish();
+        if constexpr (kPair) {
+            tmem_alloc_pair(smem_u32(&ctl->tmem_base), 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(&ctl->tmem_base), 512);
+            tmem_relinquish();
+        }
     }
     if (warp == 0) {                                   // the experts' rows and token tiles
         int64_t carry = 0;
@@ -326,79 +430,117 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync();               // both CTAs' barriers exist before any remote signal
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     volatile int* abort_flag = &ctl->abort_flag;
-    const int64_t tiles = tile_count<kMode>(p, ctl);
+    const int64_t tiles = tile_count<kMode, kPair>(p, ctl);
 
     if (warp == kProducerWarp) {
-        if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, narmed = 0;
-            bool ok = true;
-            for (int64_t u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
-                const Tile t = tile_at<kMode>(p, ctl, u);
-                const int nkb = ceil_div_i(t.depth, kBK);
-                const int nb = kMode == kWgrad ? (t.nmma + 63) / 64 : 0;     // 64-wide boxes of X
-                const uint32_t tx = kABytes + (kMode == kWgrad ? nb * 8192 : t.nmma * kBK * 2);
-                for (int kb = 0; kb < nkb; ++kb) {
+        int stage = 0;
+        uint32_t phase = 0, narmed = 0;
+        uint32_t tail_used = 0, tail_phase = 0;         // by stage: ragged last blocks armed, the parity of the last
+        bool ok = true;
+        for (int64_t u = unit; u < tiles && ok; u += units) {
+            const Tile t = tile_at<kMode, kPair>(p, ctl, u);
+            const int nkb = ceil_div_i(t.depth, kBK);
+            // this CTA's features and columns
+            const int f0 = t.f0 + static_cast<int>(rank) * kBM;
+            const int mine = t.nmma / G::kCtas, c0 = t.c0 + static_cast<int>(rank) * mine;
+            const int nb = (mine + 63) / 64;                         // wgrad: 64-wide boxes of X
+            const uint32_t bytes = kABytes + (kMode == kWgrad ? nb * 8192 : mine * kBK * 2);
+            for (int kb = 0; kb < nkb; ++kb) {
+                if (!warp_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err, 0x201)) {
+                    ok = false;
+                    break;
+                }
+                // The pair's copies count on the leader's barrier, except that a weight
+                // gradient's ragged last block counts on each CTA's own, because each
+                // zeroes its part before the leader may use it; the stage's full barrier
+                // then only turns its phase over.
+                const bool tail = kPair && kMode == kWgrad && kb + 1 == nkb && t.depth % kBK != 0;
+                if (tail) {
+                    tail_phase ^= (tail_used >> stage & 1u) << stage;
+                    tail_used |= 1u << stage;
+                }
+                if (elect_one()) {
                     const uint32_t full = smem_u32(&ctl->full[stage]);
-                    if (!mbar_wait_bounded(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err, 0x201)) {
-                        ok = false;
-                        break;
+                    uint32_t bar = kPair ? mapa_shared(full, 0) : full;
+                    if (tail) {
+                        if (leader) mbar_arrive(full);
+                        bar = smem_u32(&ctl->tail[stage]);
+                        mbar_arrive_expect_tx(bar, bytes);
+                        bar = mapa_shared(bar, rank);
+                    } else if (leader) {
+                        mbar_arrive_expect_tx(full, G::kCtas * bytes);
                     }
-                    mbar_arrive_expect_tx(full, tx);
-                    ++narmed;
-                    const uint32_t sa = smem_u32(smem + stage * kStageBytes);
+                    const uint32_t sa = smem_u32(smem + stage * G::kStageBytes);
                     const uint32_t sb = sa + kABytes;
                     const int k0 = kb * kBK;
                     if (kMode == kFwd) {
-                        tma_load_3d(sa, &p.a, full, k0, t.f0, t.e);
+                        load3<kPair>(sa, &p.a, bar, k0, f0, t.e);
                     } else if (kMode == kDgrad) {
-                        tma_load_3d(sa, &p.a, full, t.f0, k0, t.e);
-                        tma_load_3d(sa + 8192, &p.a, full, t.f0 + 64, k0, t.e);
+                        load3<kPair>(sa, &p.a, bar, f0, k0, t.e);
+                        load3<kPair>(sa + 8192, &p.a, bar, f0 + 64, k0, t.e);
                     } else {
-                        tma_load_2d(sa, &p.a, full, t.f0, t.r0 + k0);
-                        tma_load_2d(sa + 8192, &p.a, full, t.f0 + 64, t.r0 + k0);
+                        load2<kPair>(sa, &p.a, bar, f0, t.r0 + k0);
+                        load2<kPair>(sa + 8192, &p.a, bar, f0 + 64, t.r0 + k0);
                         for (int i = 0; i < nb; ++i)
-                            tma_load_2d(sb + i * 8192, &p.b[0], full, t.c0 + i * 64, t.r0 + k0);
+                            load2<kPair>(sb + i * 8192, &p.b[0], bar, c0 + i * 64, t.r0 + k0);
                     }
                     if (kMode != kWgrad) {
-                        // nmma tokens as boxes of 128, 64, 32 and 16 rows
+                        // the tokens as boxes of 128, 64, 32 and 16 rows
                         int at = 0;
-                        if (t.nmma == 256) {
-                            tma_load_2d(sb, &p.b[0], full, k0, t.c0);
+                        if (!kPair && mine == 256) {
+                            load2<kPair>(sb, &p.b[0], bar, k0, c0);
                             at = 128;
                         }
 #pragma unroll
                         for (int i = 0; i < kBoxes; ++i) {
                             const int r = 128 >> i;
-                            if (t.nmma - at >= r) {
-                                tma_load_2d(sb + at * 128, &p.b[i], full, k0, t.c0 + at);
+                            if (mine - at >= r) {
+                                load2<kPair>(sb + at * 128, &p.b[i], bar, k0, c0 + at);
                                 at += r;
                             }
                         }
                     }
-                    if (++stage == kStages) { stage = 0; phase ^= 1u; }
                 }
-            }
-            // every armed copy lands before the CTA exits, also when the MMA warp gave up first
-            for (int s = 0; s < kStages; ++s) {
-                if (narmed <= static_cast<uint32_t>(s)) continue;
-                const uint32_t times = (narmed - 1u - static_cast<uint32_t>(s)) / kStages + 1u;
-                const long long t0 = clock64();
-                while (!mbar_try_wait(smem_u32(&ctl->full[s]), (times - 1u) & 1u) && clock64() - t0 < kWaitCycles) {}
+                __syncwarp();
+                ++narmed;
+                if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
             }
         }
-    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            // every armed copy lands before the CTA exits, also when the MMA warp gave up
+            // first; the leader's barriers also count the peer's copies
+            if (leader) {
+                for (int s = 0; s < G::kStages; ++s) {
+                    if (narmed <= static_cast<uint32_t>(s)) continue;
+                    const uint32_t times = (narmed - 1u - static_cast<uint32_t>(s)) / G::kStages + 1u;
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(smem_u32(&ctl->full[s]), (times - 1u) & 1u) && clock64() - t0 < kWaitCycles) {}
+                }
+            } else if (!ok) {
+                // copies that count on the leader's barriers: time to land (~2 ms, far above
+                // a copy's latency); the closing cluster barrier keeps this CTA until the leader is done
+                const long long t0 = clock64();
+                while (clock64() - t0 < (1LL << 22)) {}
+            }
+            for (int s = 0; s < G::kStages; ++s) {
+                if (!(tail_used >> s & 1u)) continue;
+                const long long t0 = clock64();
+                while (!mbar_try_wait(smem_u32(&ctl->tail[s]), tail_phase >> s & 1u) && clock64() - t0 < kWaitCycles) {}
+            }
+        }
+    } else if (warp == kMmaWarp && leader) {
         int stage = 0;
-        uint32_t phase = 0;
+        uint32_t phase = 0, tail_phase = 0;             // tail_phase: by stage
         bool ok = true;
         int q = 0;                                      // chunks so far: accumulator ping-pong
-        for (int64_t u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
-            const Tile t = tile_at<kMode>(p, ctl, u);
+        for (int64_t u = unit; u < tiles && ok; u += units) {
+            const Tile t = tile_at<kMode, kPair>(p, ctl, u);
             const int nkb = ceil_div_i(t.depth, kBK);
-            const uint32_t idesc = instr_desc(t.nmma, kMode != kFwd, kMode == kWgrad);
+            const uint32_t idesc = instr_desc(G::kFeatures, t.nmma, kMode != kFwd, kMode == kWgrad);
             // K-major operands: 8-row groups 1 KB apart, 32 bytes per 16-wide step.
             // MN-major operands: 64-column blocks 8 KB apart, 8-row K groups 1 KB
             // apart, two of them (2 KB) per step.
@@ -407,59 +549,94 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             constexpr uint32_t a_step = (kMode == kFwd ? 32 : 2048) >> 4, b_step = (kMode == kWgrad ? 2048 : 32) >> 4;
             int in_chunk = 0;
             for (int kb = 0; kb < nkb; ++kb) {
-                if (in_chunk == 0) {
-                    bool free_ = true;
-                    if (lane == 0)
-                        free_ = mbar_wait_bounded(smem_u32(&ctl->tempty[q & 1]), ((q >> 1) & 1) ^ 1u, abort_flag, p.err, 0x202);
-                    if (!__shfl_sync(0xffffffffu, free_, 0)) { ok = false; break; }
-                    tc_fence_after();
+                if (in_chunk == 0 &&
+                    !warp_wait(smem_u32(&ctl->tempty[q & 1]), ((q >> 1) & 1) ^ 1u, abort_flag, p.err, 0x202)) {
+                    ok = false;
+                    break;
                 }
-                bool there = true;
-                if (lane == 0)
-                    there = mbar_wait_bounded(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err, 0x203);
-                if (!__shfl_sync(0xffffffffu, there, 0)) { ok = false; break; }
-                const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + kABytes;
+                if (!warp_wait(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err, 0x203)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t sa = smem_u32(smem + stage * G::kStageBytes), sb = sa + kABytes;
                 int steps = kBK / 16;
-                if (kMode == kWgrad && kb + 1 == nkb) {
-                    // the sum ends inside this block: the rows up to the next multiple of
-                    // 16 belong to another expert (or to none) and become zero in both
-                    // operands, so that not even their infinities or NaN reach the sum
-                    const int v = t.depth - kb * kBK, end = (v + 15) / 16 * 16;
-                    steps = end / 16;
-                    if (v != end) {
-                        __syncwarp();                   // the copies landed (seen by lane 0)
-                        const int boxes = 2 + (t.nmma + 63) / 64, per = (end - v) * 8;
-                        for (int i = lane; i < boxes * per; i += 32)
-                            sts_v4(sa + (i / per) * 8192 + v * 128 + (i % per) * 16, make_uint4(0, 0, 0, 0));
-                        fence_proxy_async_smem();
-                        __syncwarp();
+                if (kMode == kWgrad && kb + 1 == nkb && t.depth % kBK != 0) {   // the sum ends inside this block
+                    const int v = t.depth - kb * kBK, boxes = 2 + (t.nmma / G::kCtas + 63) / 64;
+                    steps = (v + 15) / 16;
+                    if (kPair && !warp_wait(smem_u32(&ctl->tail[stage]), tail_phase >> stage & 1u, abort_flag, p.err, 0x205)) {
+                        ok = false;
+                        break;
+                    }
+                    zero_tail(sa, boxes, v, lane);
+                    if (kPair) {
+                        bool there = mbar_wait_cluster_bounded(smem_u32(&ctl->tail_peer[stage]), tail_phase >> stage & 1u,
+                                                               abort_flag, p.err, 0x206);
+                        if (!__all_sync(0xffffffffu, there)) {
+                            ok = false;
+                            break;
+                        }
+                        tail_phase ^= 1u << stage;
                     }
                 }
-                if (lane == 0) {
-                    tc_fence_after();
+                tc_fence_after();
+                if (elect_one()) {
                     const uint32_t d = tmem + static_cast<uint32_t>((q & 1) * kBN);
-                    for (int k = 0; k < steps; ++k)
-                        umma_bf16(d, ad0 + ((sa >> 4) + k * a_step), bd0 + ((sb >> 4) + k * b_step), idesc,
-                                  (in_chunk | k) != 0 ? 1u : 0u);
-                    umma_commit(smem_u32(&ctl->empty[stage]));
+                    auto mma = [&](int k) {
+                        const uint64_t ad = ad0 + ((sa >> 4) + k * a_step), bd = bd0 + ((sb >> 4) + k * b_step);
+                        if constexpr (kPair)
+                            umma_bf16_pair(d, ad, bd, idesc, (in_chunk | k) != 0 ? 1u : 0u);
+                        else
+                            umma_bf16(d, ad, bd, idesc, (in_chunk | k) != 0 ? 1u : 0u);
+                    };
+                    if (steps == kBK / 16) {
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k) mma(k);
+                    } else {
+                        for (int k = 0; k < steps; ++k) mma(k);
+                    }
+                    commit<kPair>(smem_u32(&ctl->empty[stage]));
+                    if (in_chunk + 1 == p.chunk || kb + 1 == nkb) commit<kPair>(smem_u32(&ctl->tfull[q & 1]));
                 }
-                if (++stage == kStages) { stage = 0; phase ^= 1u; }
+                __syncwarp();
+                if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
                 if (++in_chunk == p.chunk || kb + 1 == nkb) {
-                    if (lane == 0) umma_commit(smem_u32(&ctl->tfull[q & 1]));
                     ++q;
                     in_chunk = 0;
                 }
-                __syncwarp();
             }
         }
-        if (lane == 0) {                                // all issued MMAs complete before TMEM is released
-            umma_commit(smem_u32(&ctl->drain));
+        if (elect_one()) {                              // all issued MMAs complete before TMEM is released
+            commit<kPair>(smem_u32(&ctl->drain));
+            const long long t0 = clock64();
+            while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < kWaitCycles) {}
+        }
+    } else if (warp == kMmaWarp) {
+        // the pair's second CTA: zeroes its part of each ragged last block
+        if (kMode == kWgrad) {
+            uint32_t tail_phase = 0;                    // by stage
+            int64_t blocks = 0;                         // K blocks so far: the ring's position
+            for (int64_t u = unit; u < tiles; u += units) {
+                const Tile t = tile_at<kMode, kPair>(p, ctl, u);
+                blocks += ceil_div_i(t.depth, kBK);
+                if (t.depth % kBK == 0) continue;
+                const int stage = static_cast<int>((blocks - 1) % G::kStages);
+                bool there = true;
+                if (lane == 0)
+                    there = mbar_wait_bounded(smem_u32(&ctl->tail[stage]), tail_phase >> stage & 1u, abort_flag, p.err, 0x207);
+                if (!__shfl_sync(0xffffffffu, there, 0)) break;
+                tail_phase ^= 1u << stage;
+                __syncwarp();
+                zero_tail(smem_u32(smem + stage * G::kStageBytes), 2 + (t.nmma / 2 + 63) / 64, t.depth % kBK, lane);
+                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tail_peer[stage]), 0));
+            }
+        }
+        if (lane == 0) {                                // the leader's MMAs write this CTA's accumulators
             const long long t0 = clock64();
             while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < kWaitCycles) {}
         }
     } else {
         const int quarter = warp & 3, half = warp >> 2;
-        const uint32_t buf = smem_u32(smem + kStages * kStageBytes + warp * kOutBytes);
+        const uint32_t buf = smem_u32(smem + kRingBytes + warp * kOutBytes);
         if (kMode != kWgrad) {                          // rows of no expert
             const int head = ctl->row[0], tail = ctl->row[p.experts];
             const int64_t extra = static_cast<int64_t>(head) + (p.rows - tail);
@@ -473,10 +650,12 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 }
             }
         }
+        const uint32_t tempty_leader[2] = {kPair ? mapa_shared(smem_u32(&ctl->tempty[0]), 0) : 0u,
+                                           kPair ? mapa_shared(smem_u32(&ctl->tempty[1]), 0) : 0u};
         bool ok = true;
         int q = 0;
-        for (int64_t u = blockIdx.x; u < tiles && ok; u += gridDim.x) {
-            const Tile t = tile_at<kMode>(p, ctl, u);
+        for (int64_t u = unit; u < tiles && ok; u += units) {
+            const Tile t = tile_at<kMode, kPair>(p, ctl, u);
             const int nkb = ceil_div_i(t.depth, kBK), chunks = ceil_div_i(nkb, p.chunk);
             float v[4][32];                             // this lane's row of the warp's 32-column groups
 #pragma unroll
@@ -500,11 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl->tempty[q & 1]));
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(smem_u32(&ctl->tempty[q & 1]));
+                    else
+                        mbar_arrive_cluster(tempty_leader[q & 1]);
+                }
             }
             if (!ok) break;
             if (kMode == kWgrad && t.depth == 0 && p.accumulate) continue;
-            const int f = t.f0 + quarter * 32;
+            const int f = t.f0 + static_cast<int>(rank) * kBM + quarter * 32;
             if (f >= (kMode == kWgrad ? p.n : cols)) continue;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -522,9 +706,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if constexpr (kPair) cluster_sync();               // neither CTA leaves while the other may signal it
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        if constexpr (kPair)
+            tmem_dealloc_pair(tmem, 512);
+        else
+            tmem_dealloc(tmem, 512);
     }
 }
 
@@ -584,22 +772,71 @@ struct Request {
     int experts, out_dtype, accumulate;
 };
 
-template <int kMode, bool kF32>
-cudaError_t launch_expert(const ExpertArgs& p, int64_t most_tiles, cudaStream_t s) {
-    static std::atomic<uint64_t> attr_set{0};           // one bit per device ordinal
+// CTAs of one launch: one per SM, or as many pairs as the device holds at once.
+template <int kMode, bool kF32, bool kPair>
+cudaError_t prepare_expert(int* ctas) {
+    static std::atomic<int> known[64];                  // by device ordinal; 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (!(attr_set.load() & bit)) {
-        e = cudaFuncSetAttribute(expert_kernel<kMode, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if ((*ctas = known[dev & 63].load()) > 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(expert_kernel<kMode, kF32, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    *ctas = device_sm_count();
+    if (kPair) {
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(*ctas / 2 * 2));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int pairs = 0;
+        e = cudaOccupancyMaxActiveClusters(&pairs, expert_kernel<kMode, kF32, kPair>, &cfg);
         if (e != cudaSuccess) return e;
-        attr_set.fetch_or(bit);
+        if (pairs < 1) return cudaErrorInvalidConfiguration;
+        *ctas = std::min(2 * pairs, *ctas / 2 * 2);
     }
-    const int grid = static_cast<int>(std::min<int64_t>(most_tiles, device_sm_count()));
-    expert_kernel<kMode, kF32><<<grid, kThreads, kSmemBytes, s>>>(p);
-    return cudaGetLastError();
+    known[dev & 63].store(*ctas);
+    return cudaSuccess;
 }
+
+template <int kMode, bool kF32, bool kPair>
+cudaError_t launch_expert(const ExpertArgs& p, int64_t most_tiles, cudaStream_t s) {
+    int ctas = 0;
+    const cudaError_t e = prepare_expert<kMode, kF32, kPair>(&ctas);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most_tiles * Geo<kPair>::kCtas, ctas)));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    if (kPair) {
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 2;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, expert_kernel<kMode, kF32, kPair>, p);
+}
+
+template <bool kPair>
+cudaError_t launch_mode(int mode, bool f32, const ExpertArgs& p, int64_t most_tiles, cudaStream_t s) {
+    if (mode == kFwd)
+        return f32 ? launch_expert<kFwd, true, kPair>(p, most_tiles, s) : launch_expert<kFwd, false, kPair>(p, most_tiles, s);
+    if (mode == kDgrad)
+        return f32 ? launch_expert<kDgrad, true, kPair>(p, most_tiles, s)
+                   : launch_expert<kDgrad, false, kPair>(p, most_tiles, s);
+    return f32 ? launch_expert<kWgrad, true, kPair>(p, most_tiles, s) : launch_expert<kWgrad, false, kPair>(p, most_tiles, s);
+}
+
+// -1: chosen by the call's sizes; 0 / 1: single CTAs / CTA pairs (tests, measurements).
+std::atomic<int> g_expert_pair{-1};
 
 // A float32 result's sums leave TMEM every kF32Chunk K blocks: the tensor core's
 // accumulator drops bits below its last place, always towards zero, and adding
@@ -650,6 +887,9 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
         }));
     }
     if (!get_encode()) return MO_ERR_CUDA;
+    const int forced = g_expert_pair.load();
+    const bool pair = forced >= 0 ? forced == 1 : true;
+    const int features = pair ? 2 * kBM : kBM;
     ExpertArgs p;
     bool ok;
     int64_t most_tiles;
@@ -660,14 +900,14 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
              encode(&p.o, q.out, q.out_dtype, q.k, q.n, q.experts, q.ldo, q.stride_o, 3, f32 ? 16 : 32, 32,
                     CU_TENSOR_MAP_SWIZZLE_64B);
         for (int i = 1; i < kBoxes; ++i) p.b[i] = p.b[0];
-        most_tiles = q.experts * op_ceil_div(q.n, kBM) * op_ceil_div(q.k, kBN);
+        most_tiles = q.experts * op_ceil_div(q.n, features) * op_ceil_div(q.k, kBN);
     } else {
         ok = encode(&p.a, q.b, MO_BF16, q.k, q.n, q.experts, q.ldb, q.stride_b, 3, 64, mode == kFwd ? 128 : 64, k128) &&
              encode(&p.o, q.out, q.out_dtype, cols, q.rows, 1, q.ldo, 0, 2, 32, f32 ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_NONE);
         for (int i = 0; i < kBoxes; ++i)
             ok = ok && encode(&p.b[i], q.a, MO_BF16, depth, q.rows, 1, q.lda, 0, 2, 64, 128 >> i, k128);
         // each expert may end in a tile of its own
-        most_tiles = (q.rows / kBN + std::min<int64_t>(q.experts, q.rows)) * op_ceil_div(cols, kBM);
+        most_tiles = (q.rows / kBN + std::min<int64_t>(q.experts, q.rows)) * op_ceil_div(cols, features);
     }
     if (!ok) return MO_ERR_UNSUPPORTED;                 // a stride past what a tensor map holds (2^40 bytes)
     p.offsets = q.offsets;
@@ -683,10 +923,7 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
     p.chunk = f32 ? kF32Chunk : 1 << 26;                 // more blocks than any sum has
     p.err = static_cast<int*>(ws);
     return op_status(op_traced(MO_K_EXPERT + mode, s, [&] {
-        if (mode == kFwd) return f32 ? launch_expert<kFwd, true>(p, most_tiles, s) : launch_expert<kFwd, false>(p, most_tiles, s);
-        if (mode == kDgrad)
-            return f32 ? launch_expert<kDgrad, true>(p, most_tiles, s) : launch_expert<kDgrad, false>(p, most_tiles, s);
-        return f32 ? launch_expert<kWgrad, true>(p, most_tiles, s) : launch_expert<kWgrad, false>(p, most_tiles, s);
+        return pair ? launch_mode<true>(mode, f32, p, most_tiles, s) : launch_mode<false>(mode, f32, p, most_tiles, s);
     }));
 }
 
@@ -696,6 +933,11 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
 using namespace mo;
 
 extern "C" {
+
+int mo_debug_set_expert_pair(int on) {
+    if (on < -1 || on > 1) return MO_ERR_INVALID_ARG;
+    return g_expert_pair.exchange(on) + 1;
+}
 
 int expert_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k, int experts, size_t* bytes_out) {
     if (bytes_out == nullptr) return MO_ERR_INVALID_ARG;

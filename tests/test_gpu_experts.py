@@ -9,10 +9,19 @@ import pytest
 import torch
 
 import matrix_optimizers_gb300 as mo
+from matrix_optimizers_gb300 import _binding as B
 from oracle import training as ot
 from tests.gpu_helpers import dev
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(params=[-1, 0, 1], ids=["auto", "single", "pair"], autouse=True)
+def geometry(request):
+    """Every test runs with the size-chosen tile geometry and with each of the two."""
+    prev = B.mo_debug_set_expert_pair(request.param)
+    yield request.param
+    B.mo_debug_set_expert_pair(prev)
 
 F32, BF16 = torch.float32, torch.bfloat16
 U = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
