@@ -181,14 +181,6 @@ def dtype_code(dt):
     raise MoError(MO_ERR_INVALID_ARG, f"unsupported dtype {dt}")
 
 
-def id_dtype_code(dt):
-    if dt == torch.int32:
-        return MO_I32
-    if dt == torch.int64:
-        return MO_I64
-    raise MoError(MO_ERR_INVALID_ARG, f"unsupported index dtype {dt}")
-
-
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -388,157 +380,232 @@ def plan_owners(shapes, world, ns_steps=5, w_bytes=1.0, w_flops=1.0):
     return list(owner)[:n], list(load_)[:world]
 
 
-def _need(ok, msg):
-    if not ok:
-        raise MoError(MO_ERR_INVALID_ARG, msg)
+# The training-step operators' calls are short, so their wrappers keep to few
+# Python operations: plain integers for addresses (ctypes converts them) and
+# one entry of _calls for each function, filled on first use.
+_calls = {}
 
 
-def _on_device(*tensors):
-    """Device memory, all on one device: the library takes addresses only."""
-    dev = tensors[0].device
-    _need(all(t is None or (t.is_cuda and t.device == dev) for t in tensors), "tensors must share one CUDA device")
+def _call(name):
+    f = _calls.get(name)
+    if f is None:
+        f = _calls[name] = getattr(load(), name)
+    return f
+
+
+_current_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() without building a Stream object
+_DTYPES = {torch.float32: MO_F32, torch.bfloat16: MO_BF16}
+_ID_DTYPES = {torch.int32: MO_I32, torch.int64: MO_I64}
+
+
+def _invalid(msg):
+    raise MoError(MO_ERR_INVALID_ARG, msg)
+
+
+def _op_stream(stream, tensors):
+    """Raw stream of a call whose tensors must share one CUDA device (the
+    library takes addresses only): `stream`, or that device's current one."""
+    dev = tensors[0].get_device()
+    if dev < 0:
+        _invalid("tensors must be on a CUDA device")
+    for t in tensors:
+        if t.get_device() != dev:
+            _invalid("tensors must share one CUDA device")
+    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _matrix(t, what):
+    """(address, type code, rows, cols, ld) of a float32 or bf16 matrix."""
+    if t.dim() != 2:
+        _invalid(f"{what} must be 2D")
+    (rows, cols), (ld, unit) = t.shape, t.stride()
+    if cols > 1 and unit != 1:
+        _invalid(f"{what} must have unit column stride")
+    if rows <= 1 or ld < cols and cols <= 1:
+        ld = max(ld, cols)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        _invalid(f"{what}: unsupported dtype {t.dtype}")
+    return t.data_ptr(), code, rows, cols, ld
+
+
+def _ids(t):
+    """(address, type code, count) of a vector of token ids."""
+    code = _ID_DTYPES.get(t.dtype)
+    if code is None:
+        _invalid(f"ids: unsupported dtype {t.dtype}")
+    if t.dim() != 1 or not t.is_contiguous():
+        _invalid("ids must be 1D and contiguous")
+    return t.data_ptr(), code, t.shape[0]
+
+
+def _size(name, *args):
+    out = c_size_t(0)
+    _check(_call(name)(*args, ctypes.byref(out)))
+    return out.value
+
+
+def _nbytes(ws):
+    if not ws.is_contiguous():
+        _invalid("a workspace must be contiguous")
+    return ws.numel() * ws.element_size()
 
 
 def embedding_lookup(W, ids, out, scale=1.0, stream=None):
     """out[i] = scale * W[ids[i]] for W (vocab x dim), ids (n, int32 or int64)
     and out (n x dim); ids outside the table give zeros."""
-    _on_device(W, ids, out)
-    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be 1D and contiguous")
-    _need(out.dim() == 2 and W.dim() == 2 and out.size(0) == ids.size(0) and out.size(1) == W.size(1),
-          "out must be len(ids) x dim")
-    _check(load().embedding_lookup(_ptr(W), dtype_code(W.dtype), W.size(0), W.size(1), _ld(W), _ptr(ids),
-                                   id_dtype_code(ids.dtype), ids.size(0), scale, _ptr(out), dtype_code(out.dtype),
-                                   _ld(out), _stream(stream)))
+    s = _op_stream(stream, (W, ids, out))
+    w, w_code, vocab, dim, ldw = _matrix(W, "W")
+    o, o_code, n, cols, ldo = _matrix(out, "out")
+    i, i_code, count = _ids(ids)
+    if n != count or cols != dim:
+        _invalid("out must be len(ids) x dim")
+    _check(_call("embedding_lookup")(w, w_code, vocab, dim, ldw, i, i_code, n, scale, o, o_code, ldo, s))
 
 
 def embedding_grad_workspace_bytes(n, vocab, dim):
-    out = c_size_t(0)
-    _check(load().embedding_grad_workspace_bytes(n, vocab, dim, ctypes.byref(out)))
-    return out.value
+    return _size("embedding_grad_workspace_bytes", n, vocab, dim)
 
 
 def embedding_grad(dY, ids, dW, ws, scale=1.0, accumulate=False, stream=None):
     """dW[v] (+)= scale * sum of dY[i] over ids[i] == v, dense (vocab x dim);
     a contiguous float32 dW is what make_tail takes as g."""
-    _on_device(dW, dY, ids, ws)
-    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be 1D and contiguous")
-    _need(dY.dim() == 2 and dW.dim() == 2 and dY.size(0) == ids.size(0) and dY.size(1) == dW.size(1),
-          "dY must be len(ids) x dim")
-    _check(load().embedding_grad(_ptr(dY), dtype_code(dY.dtype), dY.size(0), dW.size(1), _ld(dY), _ptr(ids),
-                                 id_dtype_code(ids.dtype), dW.size(0), scale, _ptr(dW), dtype_code(dW.dtype), _ld(dW),
-                                 1 if accumulate else 0, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    s = _op_stream(stream, (dY, ids, dW, ws))
+    y, y_code, n, dim, ldy = _matrix(dY, "dY")
+    w, w_code, vocab, cols, ldw = _matrix(dW, "dW")
+    i, i_code, count = _ids(ids)
+    if n != count or cols != dim:
+        _invalid("dY must be len(ids) x dim")
+    _check(_call("embedding_grad")(y, y_code, n, dim, ldy, i, i_code, vocab, scale, w, w_code, ldw,
+                                   1 if accumulate else 0, ws.data_ptr(), _nbytes(ws), s))
 
 
 def expert_linear_workspace_bytes(rows, n, k, experts):
-    out = c_size_t(0)
-    _check(load().expert_linear_workspace_bytes(rows, n, k, experts, ctypes.byref(out)))
-    return out.value
+    return _size("expert_linear_workspace_bytes", rows, n, k, experts)
 
 
-def _stack(t):
-    """(ld, stride) of a stack of matrices (experts x rows x cols)."""
-    _need(t.dim() == 3 and (t.size(2) <= 1 or t.stride(2) == 1), "expert matrices must be 3D with unit column stride")
-    ld = t.stride(1) if t.size(1) > 1 else max(t.size(2), t.stride(1))
-    return ld, t.stride(0) if t.size(0) > 1 else max(t.size(1) * ld, t.stride(0))
-
-
-def _bf16(*tensors):
-    _need(all(t.dtype == torch.bfloat16 for t in tensors), "operands must be bfloat16")
+def _stack(t, what):
+    """(address, type code, experts, rows, cols, ld, stride) of a stack of matrices."""
+    if t.dim() != 3:
+        _invalid(f"{what} must be 3D")
+    (experts, rows, cols), (stride, ld, unit) = t.shape, t.stride()
+    if cols > 1 and unit != 1:
+        _invalid(f"{what} must have unit column stride")
+    if rows <= 1:
+        ld = max(ld, cols)
+    if experts <= 1:
+        stride = max(stride, rows * ld)
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        _invalid(f"{what}: unsupported dtype {t.dtype}")
+    return t.data_ptr(), code, experts, rows, cols, ld, stride
 
 
 def _offsets(offsets, experts):
-    _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous() and
-          offsets.numel() == experts + 1, "offsets must be experts + 1 contiguous int32")
-    return _ptr(offsets)
+    if offsets.dtype != torch.int32 or offsets.shape != (experts + 1,) or not offsets.is_contiguous():
+        _invalid("offsets must be experts + 1 contiguous int32")
+    return offsets.data_ptr()
 
 
 def expert_linear(X, W, offsets, Y, ws, stream=None):
     """Y[r] = X[r] W_e^T for the rows r of expert e (offsets[e] .. offsets[e+1] - 1):
     X rows x k and W experts x n x k in bf16, Y rows x n float32 or bf16."""
-    _on_device(X, W, offsets, Y, ws)
-    _bf16(X, W)
-    ldw, stride = _stack(W)
-    _need(X.dim() == 2 and Y.dim() == 2 and X.size(0) == Y.size(0) and X.size(1) == W.size(2) and
-          Y.size(1) == W.size(1), "X must be rows x k and Y rows x n of W's experts x n x k")
-    _check(load().expert_linear(_ptr(X), _ld(X), _ptr(W), ldw, stride, _offsets(offsets, W.size(0)), X.size(0),
-                                W.size(1), W.size(2), W.size(0), _ptr(Y), dtype_code(Y.dtype), _ld(Y), _ptr(ws),
-                                ws.numel() * ws.element_size(), _stream(stream)))
+    s = _op_stream(stream, (X, W, offsets, Y, ws))
+    x, x_code, rows, k, ldx = _matrix(X, "X")
+    y, y_code, y_rows, y_cols, ldy = _matrix(Y, "Y")
+    w, w_code, experts, n, w_cols, ldw, stride = _stack(W, "W")
+    if x_code != MO_BF16 or w_code != MO_BF16:
+        _invalid("operands must be bfloat16")
+    if y_rows != rows or w_cols != k or y_cols != n:
+        _invalid("X must be rows x k and Y rows x n of W's experts x n x k")
+    _check(_call("expert_linear")(x, ldx, w, ldw, stride, _offsets(offsets, experts), rows, n, k, experts, y, y_code,
+                                  ldy, ws.data_ptr(), _nbytes(ws), s))
 
 
 def expert_linear_dgrad(dY, W, offsets, dX, ws, stream=None):
     """dX[r] = dY[r] W_e: the input's gradient of expert_linear."""
-    _on_device(dY, W, offsets, dX, ws)
-    _bf16(dY, W)
-    ldw, stride = _stack(W)
-    _need(dY.dim() == 2 and dX.dim() == 2 and dY.size(0) == dX.size(0) and dY.size(1) == W.size(1) and
-          dX.size(1) == W.size(2), "dY must be rows x n and dX rows x k of W's experts x n x k")
-    _check(load().expert_linear_dgrad(_ptr(dY), _ld(dY), _ptr(W), ldw, stride, _offsets(offsets, W.size(0)),
-                                      dY.size(0), W.size(1), W.size(2), W.size(0), _ptr(dX), dtype_code(dX.dtype),
-                                      _ld(dX), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+    s = _op_stream(stream, (dY, W, offsets, dX, ws))
+    y, y_code, rows, n, ldy = _matrix(dY, "dY")
+    x, x_code, x_rows, k, ldx = _matrix(dX, "dX")
+    w, w_code, experts, w_rows, w_cols, ldw, stride = _stack(W, "W")
+    if y_code != MO_BF16 or w_code != MO_BF16:
+        _invalid("operands must be bfloat16")
+    if x_rows != rows or w_rows != n or w_cols != k:
+        _invalid("dY must be rows x n and dX rows x k of W's experts x n x k")
+    _check(_call("expert_linear_dgrad")(y, ldy, w, ldw, stride, _offsets(offsets, experts), rows, n, k, experts, x,
+                                        x_code, ldx, ws.data_ptr(), _nbytes(ws), s))
 
 
 def expert_linear_wgrad(dY, X, offsets, dW, ws, accumulate=False, stream=None):
     """dW[e] (+)= dY_e^T X_e: the weights' gradients of expert_linear; each dW[e]
     is the G of one make_matrix."""
-    _on_device(dY, X, offsets, dW, ws)
-    _bf16(dY, X)
-    ld, stride = _stack(dW)
-    _need(dY.dim() == 2 and X.dim() == 2 and dY.size(0) == X.size(0) and dY.size(1) == dW.size(1) and
-          X.size(1) == dW.size(2), "dY must be rows x n and X rows x k of dW's experts x n x k")
-    _check(load().expert_linear_wgrad(_ptr(dY), _ld(dY), _ptr(X), _ld(X), _offsets(offsets, dW.size(0)), X.size(0),
-                                      dW.size(1), dW.size(2), dW.size(0), _ptr(dW), dtype_code(dW.dtype), ld, stride,
-                                      1 if accumulate else 0, _ptr(ws), ws.numel() * ws.element_size(),
-                                      _stream(stream)))
+    s = _op_stream(stream, (dY, X, offsets, dW, ws))
+    y, y_code, rows, n, ldy = _matrix(dY, "dY")
+    x, x_code, x_rows, k, ldx = _matrix(X, "X")
+    w, w_code, experts, w_rows, w_cols, ldw, stride = _stack(dW, "dW")
+    if y_code != MO_BF16 or x_code != MO_BF16:
+        _invalid("operands must be bfloat16")
+    if x_rows != rows or w_rows != n or w_cols != k:
+        _invalid("dY must be rows x n and X rows x k of dW's experts x n x k")
+    _check(_call("expert_linear_wgrad")(y, ldy, x, ldx, _offsets(offsets, experts), rows, n, k, experts, w, w_code,
+                                        ldw, stride, 1 if accumulate else 0, ws.data_ptr(), _nbytes(ws), s))
 
 
 def _distill(logits, idx, teacher, temperature, row_weight, grad_scale):
-    _need(logits.dim() == 2 and idx.dim() == 2 and idx.shape == teacher.shape and idx.size(0) == logits.size(0) and
-          idx.is_contiguous() and teacher.is_contiguous(), "idx and teacher must be contiguous, rows x top")
+    p, code, n, vocab, ld = _matrix(logits, "logits")
+    t_code, i_code = _DTYPES.get(teacher.dtype), _ID_DTYPES.get(idx.dtype)
+    if t_code is None or i_code is None:
+        _invalid("teacher must be float32 or bfloat16, idx int32 or int64")
+    if (idx.dim() != 2 or idx.shape != teacher.shape or idx.shape[0] != n or not idx.is_contiguous() or
+            not teacher.is_contiguous()):
+        _invalid("idx and teacher must be contiguous, rows x top")
+    w = None
     if row_weight is not None:
-        _need(row_weight.dtype == torch.float32 and row_weight.is_contiguous() and
-              tuple(row_weight.shape) == (logits.size(0),), "row_weight must be contiguous float32, one per row")
-    return mo_distill(logits.size(0), logits.size(1), _ld(logits), idx.size(1), dtype_code(logits.dtype),
-                      id_dtype_code(idx.dtype), dtype_code(teacher.dtype), temperature, grad_scale,
-                      logits.data_ptr(), idx.data_ptr(), teacher.data_ptr(),
-                      None if row_weight is None else row_weight.data_ptr())
+        if row_weight.dtype != torch.float32 or row_weight.shape != (n,) or not row_weight.is_contiguous():
+            _invalid("row_weight must be contiguous float32, one per row")
+        w = row_weight.data_ptr()
+    return mo_distill(n, vocab, ld, idx.shape[1], code, i_code, t_code, temperature, grad_scale, p, idx.data_ptr(),
+                      teacher.data_ptr(), w)
 
 
 def _f32_out(t, shape, name):
-    _need(t.dtype == torch.float32 and t.is_contiguous() and tuple(t.shape) == shape,
-          f"{name} must be contiguous float32 of shape {shape}")
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
+        _invalid(f"{name} must be contiguous float32 of shape {shape}")
+    return t.data_ptr()
+
+
+def _dlogits(dlogits, logits):
+    if dlogits.shape != logits.shape:
+        _invalid("dlogits must have the logits' shape")
+    p, code, _, _, ld = _matrix(dlogits, "dlogits")
+    return p, code, ld
 
 
 def distill_topk_loss(logits, idx, teacher, loss, stats, temperature=1.0, row_weight=None, stream=None):
     """Per-row distillation loss from the teacher's top logits (include/matrixopt.h)
     and the row statistics distill_topk_grad takes (rows x 2)."""
-    _on_device(logits, idx, teacher, loss, stats, row_weight)
+    s = _op_stream(stream, (logits, idx, teacher, loss, stats) + (() if row_weight is None else (row_weight,)))
     d = _distill(logits, idx, teacher, temperature, row_weight, 1.0)
-    _f32_out(loss, (logits.size(0),), "loss")
-    _f32_out(stats, (logits.size(0), 2), "stats")
-    _check(load().distill_topk_loss(ctypes.byref(d), _ptr(loss), _ptr(stats), _stream(stream)))
+    _check(_call("distill_topk_loss")(d, _f32_out(loss, (d.n,), "loss"), _f32_out(stats, (d.n, 2), "stats"), s))
 
 
 def distill_topk_grad(logits, idx, teacher, stats, dlogits, temperature=1.0, row_weight=None, grad_scale=1.0,
                       stream=None):
     """The loss's gradient by the logits, from distill_topk_loss's statistics;
     dlogits may be the logits themselves."""
-    _on_device(logits, idx, teacher, stats, dlogits, row_weight)
+    s = _op_stream(stream, (logits, idx, teacher, stats, dlogits) + (() if row_weight is None else (row_weight,)))
     d = _distill(logits, idx, teacher, temperature, row_weight, grad_scale)
-    _f32_out(stats, (logits.size(0), 2), "stats")
-    _need(dlogits.shape == logits.shape, "dlogits must have the logits' shape")
-    _check(load().distill_topk_grad(ctypes.byref(d), _ptr(stats), _ptr(dlogits), dtype_code(dlogits.dtype),
-                                    _ld(dlogits), _stream(stream)))
+    g, code, ld = _dlogits(dlogits, logits)
+    _check(_call("distill_topk_grad")(d, _f32_out(stats, (d.n, 2), "stats"), g, code, ld, s))
 
 
 def distill_topk_loss_grad(logits, idx, teacher, loss, dlogits, temperature=1.0, row_weight=None, grad_scale=1.0,
                            stream=None):
     """Loss and gradient in one pass over the logits; dlogits may be the logits."""
-    _on_device(logits, idx, teacher, loss, dlogits, row_weight)
+    s = _op_stream(stream, (logits, idx, teacher, loss, dlogits) + (() if row_weight is None else (row_weight,)))
     d = _distill(logits, idx, teacher, temperature, row_weight, grad_scale)
-    _f32_out(loss, (logits.size(0),), "loss")
-    _need(dlogits.shape == logits.shape, "dlogits must have the logits' shape")
-    _check(load().distill_topk_loss_grad(ctypes.byref(d), _ptr(loss), _ptr(dlogits), dtype_code(dlogits.dtype),
-                                         _ld(dlogits), _stream(stream)))
+    g, code, ld = _dlogits(dlogits, logits)
+    _check(_call("distill_topk_loss_grad")(d, _f32_out(loss, (d.n,), "loss"), g, code, ld, s))
 
 
 def mo_check_device_status(ws, stream=None):

@@ -14,9 +14,15 @@
 // rows, which the block of the chunk where the run starts adds up in order.
 // Equal chunks keep the work balanced when a few tokens make up most of a batch,
 // as they do in text.
+#include <cooperative_groups.h>
+
+#include <atomic>
+
 #include "train_common.cuh"
 
 namespace mo {
+
+namespace cg = cooperative_groups;
 
 using bf16 = __nv_bfloat16;
 
@@ -25,60 +31,80 @@ namespace {
 // ------------------------------------------------------------------- lookup
 constexpr int kLookupThreads = 256;
 
-// One 16-byte (or, where a row is not 16-byte aligned, one-element) piece per
-// thread and step; consecutive threads take consecutive pieces of a row.
-template <typename W, typename O>
-__global__ void __launch_bounds__(kLookupThreads)
-lookup_kernel(const W* __restrict__ w, int64_t vocab, int64_t dim, int64_t ldw, const void* __restrict__ ids,
-              int id_dtype, int64_t n, float scale, O* __restrict__ out, int64_t ldo, int wide) {
+// The 16 bytes at p (a full access), of which `valid` elements are real, as the elements' own bits.
+template <bool kWide, typename W>
+__device__ __forceinline__ uint4 load_piece(const W* p, int valid) {
     constexpr int V = Elem<W>::kVec;
-    const int64_t groups = (dim + V - 1) / V;
-    const int64_t total = n * groups;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * kLookupThreads;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x; t < total; t += step) {
-        const int64_t i = t / groups, c = (t - i * groups) * V;
-        const int64_t id = load_id(ids, id_dtype, i, vocab);
-        const W* src = w + id * ldw + c;
-        O* dst = out + i * ldo + c;
-        const int nv = static_cast<int>(dim - c < V ? dim - c : V);
-        if (nv == V) {
-            float v[V];
-            if (id < 0) {
+    if (kWide && valid >= V) return __ldg(reinterpret_cast<const uint4*>(p));
+    float v[V];
 #pragma unroll
-                for (int k = 0; k < V; ++k) v[k] = 0.f;
-            } else if (wide) {
-                unpack16(__ldg(reinterpret_cast<const uint4*>(src)), v);
-            } else {
+    for (int k = 0; k < V; ++k) v[k] = k < valid ? Elem<W>::to_float(p[k]) : 0.f;
+    return pack16(v);
+}
+
+// Eight columns per thread and step, so that a bf16 result leaves in 16-byte
+// stores.  A row belongs to 2^row_bits consecutive threads (as many as it has
+// such pieces, at most a block), which take its pieces in turn.  kWide: rows start
+// on 16-byte boundaries and hold whole pieces, so that a step is loads, multiplies
+// and stores alone: with bounds checks in it the instructions, not the bytes, set
+// the time (32768 rows of 4096 float32 to bf16: 127 us; more rows or pieces in
+// flight per thread, which cost more instructions, were slower still).
+template <typename W, typename O, bool kWide>
+__global__ void __launch_bounds__(kLookupThreads)
+lookup_kernel(const W* __restrict__ w, int64_t vocab, int dim, int64_t ldw, const void* __restrict__ ids, int id_dtype,
+              int64_t n, float scale, O* __restrict__ out, int64_t ldo, int row_bits) {
+    constexpr int V = Elem<W>::kVec;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * (kLookupThreads >> row_bits) + (threadIdx.x >> row_bits);
+    if (i >= n) return;
+    const int64_t id = load_id(ids, id_dtype, i, vocab);
+    const W* src = w + id * ldw;
+    O* dst = out + i * ldo;
+    const int step = 8 << row_bits, c0 = static_cast<int>(threadIdx.x & ((1 << row_bits) - 1)) * 8;
+    if (id < 0) {                                    // padding: +0 whatever the scale
+        for (int c = c0; c < dim; c += step)
+            for (int k = 0; k < 8 && c + k < dim; ++k) dst[c + k] = Elem<O>::from_float(0.f);
+        return;
+    }
+    if (kWide) {
+#pragma unroll 2
+        for (int c = c0; c < dim; c += step) {
+            float v[8];
 #pragma unroll
-                for (int k = 0; k < V; ++k) v[k] = Elem<W>::to_float(src[k]);
+            for (int q = 0; q < 8 / V; ++q) {
+                float x[V];
+                unpack16(__ldg(reinterpret_cast<const uint4*>(src + c) + q), x);
+#pragma unroll
+                for (int k = 0; k < V; ++k) v[q * V + k] = x[k] * scale;
             }
-            // a padding row is +0 whatever the scale
-#pragma unroll
-            for (int k = 0; k < V; ++k) v[k] = id < 0 ? 0.f : v[k] * scale;
-            store_run<O, V>(dst, v, wide);
-        } else {
-            for (int k = 0; k < nv; ++k)
-                dst[k] = Elem<O>::from_float(id < 0 ? 0.f : Elem<W>::to_float(src[k]) * scale);
+            store_run<O, 8>(dst + c, v, true);
         }
+    } else {
+        for (int c = c0; c < dim; c += step)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + k < dim) dst[c + k] = Elem<O>::from_float(Elem<W>::to_float(src[c + k]) * scale);
     }
 }
 
 template <typename W, typename O>
 cudaError_t launch_lookup(const void* w, int64_t vocab, int64_t dim, int64_t ldw, const void* ids, int id_dtype,
                           int64_t n, float scale, void* out, int64_t ldo, cudaStream_t s) {
-    constexpr int V = Elem<W>::kVec;
-    const bool wide = op_aligned(w, 16) && (ldw * sizeof(W)) % 16 == 0 && op_aligned(out, V * sizeof(O) < 16 ? 8 : 16) &&
-                      (ldo * sizeof(O)) % (V * sizeof(O) < 16 ? 8 : 16) == 0;
-    const int64_t blocks = op_ceil_div(n * op_ceil_div(dim, V), kLookupThreads);
-    const int grid = static_cast<int>(blocks < 32768 ? blocks : 32768);
-    lookup_kernel<W, O><<<grid, kLookupThreads, 0, s>>>(static_cast<const W*>(w), vocab, dim, ldw, ids, id_dtype, n,
-                                                        scale, static_cast<O*>(out), ldo, wide);
-    return cudaGetLastError();
+    const bool wide = dim % 8 == 0 && op_aligned(w, 16) && (ldw * sizeof(W)) % 16 == 0 && op_aligned(out, 16) &&
+                      (ldo * sizeof(O)) % 16 == 0;
+    int row_bits = 0;
+    while ((1 << row_bits) < kLookupThreads && (int64_t(8) << row_bits) < dim) ++row_bits;
+    const unsigned grid = static_cast<unsigned>(op_ceil_div(n, kLookupThreads >> row_bits));
+    auto go = [&](auto kernel) {
+        kernel<<<grid, kLookupThreads, 0, s>>>(static_cast<const W*>(w), vocab, static_cast<int>(dim), ldw, ids, id_dtype, n,
+                                               scale, static_cast<O*>(out), ldo, row_bits);
+        return cudaGetLastError();
+    };
+    return wide ? go(lookup_kernel<W, O, true>) : go(lookup_kernel<W, O, false>);
 }
 
 // ------------------------------------------------ stable radix sort by token
 // Keys 0 .. vocab - 1, and vocab for a dropped position, in passes of at most
-// kDigitBits bits.  A pass counts the digits of each tile of positions, then
+// kDigitBits bits.  Beyond one cluster's reach (below) a pass counts the digits of each tile of positions, then
 // each tile finds where its digits start (all smaller digits of all tiles,
 // plus equal digits of earlier tiles) and scatters in order.
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
@@ -93,8 +119,21 @@ struct SortPass {
     uint32_t* pos_out;
     uint32_t* counts;          // [tiles][digits]
     int64_t n, vocab;
-    int shift, digits, tiles, rounds;   // a tile holds rounds * kSortThreads positions
+    int shift, digit_bits, digits, tiles, rounds;   // a tile holds rounds * kSortThreads positions
 };
+
+// The lanes with `in` whose digit equals this lane's, by one vote per bit
+// (match.any took most of the sort's time).
+__device__ __forceinline__ uint32_t same_digit(uint32_t d, bool in, int bits) {
+    uint32_t same = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b) {
+        const bool set = d >> b & 1u;
+        const uint32_t votes = __ballot_sync(0xffffffffu, set);
+        if (b < bits) same &= set ? votes : ~votes;
+    }
+    return same;
+}
 
 __device__ __forceinline__ uint32_t sort_key(const SortPass& p, int64_t i) {
     if (p.keys_in != nullptr) return p.keys_in[i];
@@ -165,8 +204,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const __grid
         const int64_t i = first + r * 32;
         const bool in = i < p.n;
         const uint32_t key = in ? sort_key(p, i) : 0;
-        const uint32_t d = in ? (key >> p.shift) & (p.digits - 1) : 0xffffffffu;
-        const uint32_t same = __match_any_sync(0xffffffffu, d);
+        const uint32_t d = (key >> p.shift) & (p.digits - 1);
+        const uint32_t same = same_digit(d, in, p.digit_bits);
         const uint32_t rank = __popc(same & ((1u << lane) - 1u));
         uint32_t at = 0;
         if (in) at = hist[warp][d] + rank;
@@ -180,11 +219,174 @@ __global__ void __launch_bounds__(kSortThreads) sort_scatter_kernel(const __grid
     }
 }
 
+// Up to 128 K positions of up to 2^18 - 1 tokens: both passes in one launch of one
+// cluster, whose CTAs keep the elements in shared memory and exchange digit counts
+// and scattered elements through distributed shared memory.  An element is one
+// word, its position with the digit that is still to be sorted by above it; the
+// key written out at the end is read again from the ids.  Bound by latency: the
+// votes and counter updates of a round, and the scattered words.
+constexpr int kClusterThreads = 1024, kClusterWarps = kClusterThreads / 32;
+constexpr int kClusterMax = 16;                      // CTAs of a cluster
+constexpr int kClusterRounds = 8;                    // positions per thread, at most
+constexpr int kClusterKeys = kClusterThreads * kClusterRounds;
+constexpr int kPosBits = 17;
+constexpr int64_t kClusterSortMax = static_cast<int64_t>(kClusterMax) * kClusterKeys;
+constexpr int64_t kClusterVocabMax = (int64_t(1) << (2 * kDigitBits)) - 1;
+static_assert(kClusterSortMax <= (int64_t(1) << kPosBits) && kPosBits + kDigitBits <= 32, "one word per element");
+
+struct ClusterSmem {
+    uint32_t elem[kClusterKeys];
+    uint16_t hist[kClusterWarps][kDigits];           // digits of each warp, then where the warp's first one goes in the CTA's run
+    uint32_t total[kDigits];                         // digits of this CTA
+    uint32_t base[kDigits];
+    uint32_t scan[kClusterWarps];
+};
+static_assert(sizeof(ClusterSmem) <= 232448, "shared memory");
+
+template <int kRounds>
+__global__ void __launch_bounds__(kClusterThreads, 1)
+cluster_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, int digit_bits, uint32_t* keys_out,
+                    uint32_t* pos_out) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    ClusterSmem& sm = *reinterpret_cast<ClusterSmem*>(smem_raw);
+    cg::cluster_group cluster = cg::this_cluster();
+    const int ctas = static_cast<int>(cluster.num_blocks()), me = static_cast<int>(cluster.block_rank());
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int per = kRounds * kClusterThreads;                    // positions of a CTA: a power of two
+    const int mine = min(per, max(0, n - me * per));                  // how many this CTA holds
+    const uint32_t digits = 1u << digit_bits, pos_mask = (1u << kPosBits) - 1u;
+    auto key_of = [&](uint32_t pos) {
+        const int64_t id = load_id(ids, id_dtype, pos, vocab);
+        return static_cast<uint32_t>(id < 0 ? vocab : id);
+    };
+    for (int pass = 0; pass < 2; ++pass) {
+        uint32_t* h = reinterpret_cast<uint32_t*>(&sm.hist[0][0]);
+        for (int d = threadIdx.x; d < kClusterWarps * kDigits / 2; d += kClusterThreads) h[d] = 0;
+        // a warp takes rounds * 32 consecutive elements, 32 at a time: their order is warp, round, lane
+        uint32_t key[kRounds];                       // pass 0: the key; pass 1: the element
+        uint16_t rank[kRounds];
+        const int i0 = warp * kRounds * 32 + lane;
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int i = i0 + r * 32;
+            key[r] = 0;
+            if (i < mine)
+                key[r] = pass == 0 ? key_of(static_cast<uint32_t>(me * per + i)) : sm.elem[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const bool in = i0 + r * 32 < mine;
+            const uint32_t d = pass == 0 ? key[r] & (digits - 1) : key[r] >> kPosBits;
+            const uint32_t same = same_digit(d, in, digit_bits);
+            const uint32_t before = __popc(same & ((1u << lane) - 1u));
+            const uint16_t seen = in ? sm.hist[warp][d] : 0;
+            rank[r] = static_cast<uint16_t>(seen + before);
+            __syncwarp();
+            if (in && before == 0) sm.hist[warp][d] = static_cast<uint16_t>(seen + __popc(same));
+            __syncwarp();
+        }
+        __syncthreads();
+        if (threadIdx.x < kDigits) {
+            uint32_t run = 0;
+#pragma unroll 8
+            for (int w = 0; w < kClusterWarps; ++w) {
+                const uint16_t c = sm.hist[w][threadIdx.x];
+                sm.hist[w][threadIdx.x] = static_cast<uint16_t>(run);
+                run += c;
+            }
+            sm.total[threadIdx.x] = run;
+        }
+        cluster.sync();
+        uint32_t all = 0, before = 0;
+        if (threadIdx.x < kDigits) {
+#pragma unroll
+            for (int c = 0; c < kClusterMax; ++c) {
+                const uint32_t t = c < ctas ? cluster.map_shared_rank(&sm.total[0], c)[threadIdx.x] : 0;
+                if (c < me) before += t;
+                all += t;
+            }
+        }
+        uint32_t incl = all;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sm.scan[warp] = incl;
+        __syncthreads();
+        if (threadIdx.x < kDigits) {
+            uint32_t off = 0;
+#pragma unroll
+            for (int w = 0; w < kDigits / 32; ++w) off += w < warp ? sm.scan[w] : 0;
+            sm.base[threadIdx.x] = off + incl - all + before;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+            const int i = i0 + r * 32;
+            if (i >= mine) continue;
+            const uint32_t d = pass == 0 ? key[r] & (digits - 1) : key[r] >> kPosBits;
+            const uint32_t to = sm.base[d] + sm.hist[warp][d] + rank[r];
+            if (pass == 0) {
+                const uint32_t e = (key[r] >> digit_bits) << kPosBits | static_cast<uint32_t>(me * per + i);
+                cluster.map_shared_rank(&sm.elem[0], static_cast<int>(to / per))[to % per] = e;
+            } else {
+                const uint32_t pos = key[r] & pos_mask;
+                keys_out[to] = key_of(pos);
+                pos_out[to] = pos;
+            }
+        }
+        // pass 0: the scattered elements have arrived; pass 1: no CTA reads another's counts any more
+        if (pass == 0) cluster.sync();
+    }
+    cluster.sync();
+}
+
+template <int kRounds>
+cudaError_t launch_cluster_sort(const void* ids, int id_dtype, int64_t n, int64_t vocab, uint32_t* keys, uint32_t* pos,
+                                cudaStream_t s) {
+    // spread over the cluster first, then over rounds
+    if (kRounds < kClusterRounds && n > static_cast<int64_t>(kClusterMax) * kRounds * kClusterThreads)
+        return launch_cluster_sort<kRounds < kClusterRounds ? 2 * kRounds : kRounds>(ids, id_dtype, n, vocab, keys, pos, s);
+    static std::atomic<uint64_t> attr_set{0};        // one bit per device ordinal
+    const auto kernel = cluster_sort_kernel<kRounds>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (!(attr_set.load() & bit)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(ClusterSmem));
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        attr_set.fetch_or(bit);
+    }
+    int bits = 2;                                    // keys 0 .. vocab, in two digits
+    while ((int64_t(1) << bits) <= vocab) ++bits;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    const unsigned ctas = static_cast<unsigned>(op_ceil_div(n, kRounds * kClusterThreads));
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kClusterThreads);
+    cfg.dynamicSmemBytes = sizeof(ClusterSmem);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, ids, id_dtype, static_cast<int>(n), vocab, (bits + 1) / 2, keys, pos);
+}
+
 // -------------------------------------------------------- sums of sorted runs
-constexpr int kChunk = 64;            // sorted positions per block
+constexpr int kMaxChunk = 64;         // sorted positions per block, at most
 constexpr int kGradThreads = 128;     // columns per block: 128 x one 16-byte access
-constexpr int kZeroRows = 64;         // table rows per block of the zero fill
+constexpr int kMaxZeroRows = 64;      // table rows per block of the zero fill, at most
 constexpr int kAhead = 8;             // rows in flight per thread
+// Chunks halve (down to 8) until the sums have this many blocks: a small batch is
+// bound by the latency of its rows, a large one by their bytes.
+constexpr int64_t kGradBlocks = 600;
 
 struct GradArgs {
     const void* dy;
@@ -195,7 +397,8 @@ struct GradArgs {
     int64_t ldw;
     float* part;                      // [chunk][2][dim]: a run's rows in a chunk it enters from before, or leaves
     float scale;
-    int accumulate, wide_in, wide_out;
+    int accumulate, wide_out;
+    int chunk, zero_rows;             // positions per chunk, table rows per zero-fill block
     int64_t chunks, sum_blocks;       // sum_blocks = chunks * column slabs; zero-fill blocks follow
 };
 
@@ -218,34 +421,54 @@ __device__ __forceinline__ void write_row(const GradArgs& a, uint32_t key, int64
     }
 }
 
-// First sorted position whose key is not below v.
-__device__ __forceinline__ int64_t lower_bound_key(const uint32_t* keys, int64_t n, int64_t v) {
-    int64_t lo = 0, hi = n;
+// First sorted position in [lo, hi] whose key is not below v.
+__device__ __forceinline__ int64_t lower_bound_key(const uint32_t* keys, int64_t lo, int64_t hi, int64_t v) {
     while (lo < hi) {
         const int64_t mid = (lo + hi) >> 1;
         if (keys[mid] < v) lo = mid + 1; else hi = mid;
     }
     return lo;
 }
+// The same by a whole warp, 32 probes at a time.
+__device__ __forceinline__ int64_t warp_lower_bound_key(const uint32_t* keys, int64_t n, int64_t v) {
+    int64_t lo = 0, hi = n;                           // the answer lies in [lo, hi]
+    while (lo < hi) {
+        const int64_t step = (hi - lo + 31) / 32, at = lo + (threadIdx.x & 31) * step;
+        const uint32_t below = __ballot_sync(0xffffffffu, at < hi && keys[at] < v);   // a prefix of the lanes
+        const int c = __popc(below);
+        if (c == 0) return lo;
+        const int64_t nlo = lo + (c - 1) * step + 1, nhi = lo + c * step;
+        lo = nlo;
+        hi = nhi < hi ? nhi : hi;
+    }
+    return lo;
+}
 
-template <typename T, typename D>
+template <typename T, typename D, bool kWide>
 __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_constant__ GradArgs a) {
     constexpr int V = Elem<T>::kVec;
     if (blockIdx.x >= a.sum_blocks) {                // rows of absent tokens: zeros
-        const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - a.sum_blocks) * kZeroRows;
-        __shared__ uint8_t present[kZeroRows];
-        for (int r = threadIdx.x; r < kZeroRows; r += kGradThreads) {
+        const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - a.sum_blocks) * a.zero_rows;
+        __shared__ uint8_t present[kMaxZeroRows];
+        __shared__ int64_t range[2];
+        if (threadIdx.x < 64) {                       // the positions of the block's tokens
+            const int w = threadIdx.x >> 5;
+            const int64_t at = warp_lower_bound_key(a.keys, a.n, r0 + (w ? a.zero_rows : 0));
+            if ((threadIdx.x & 31) == 0) range[w] = at;
+        }
+        __syncthreads();
+        for (int r = threadIdx.x; r < a.zero_rows; r += kGradThreads) {
             const int64_t v = r0 + r;
             uint8_t is = 1;
             if (v < a.vocab) {
-                const int64_t at = lower_bound_key(a.keys, a.n, v);
-                is = at < a.n && a.keys[at] == v;
+                const int64_t at = lower_bound_key(a.keys, range[0], range[1], v);
+                is = at < range[1] && a.keys[at] == v;
             }
             present[r] = is;
         }
         __syncthreads();
         constexpr int Z = Elem<D>::kVec;
-        for (int r = 0; r < kZeroRows; ++r) {
+        for (int r = 0; r < a.zero_rows; ++r) {
             if (present[r]) continue;
             D* row = static_cast<D*>(a.dw) + (r0 + r) * a.ldw;
             if (a.wide_out) {
@@ -259,10 +482,10 @@ __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_con
         }
         return;
     }
-    __shared__ uint32_t skey[kChunk + 2], spos[kChunk];      // skey[0], skey[len + 1]: the neighbours' keys
+    __shared__ uint32_t skey[kMaxChunk + 2], spos[kMaxChunk];   // skey[0], skey[len + 1]: the neighbours' keys
     const int64_t chunk = blockIdx.x % a.chunks, slab = blockIdx.x / a.chunks;
-    const int64_t p0 = chunk * kChunk;
-    const int len = static_cast<int>(a.n - p0 < kChunk ? a.n - p0 : kChunk);
+    const int64_t p0 = chunk * a.chunk;
+    const int len = static_cast<int>(a.n - p0 < a.chunk ? a.n - p0 : a.chunk);
     const uint32_t none = 0xffffffffu, dropped = static_cast<uint32_t>(a.vocab);
     for (int i = threadIdx.x; i < len + 2; i += kGradThreads) {
         const int64_t q = p0 + i - 1;
@@ -274,31 +497,26 @@ __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_con
     if (c >= a.dim) return;
     const int nv = static_cast<int>(a.dim - c < V ? a.dim - c : V);
     const T* dy = static_cast<const T*>(a.dy) + c;
-    const bool wide = a.wide_in && nv == V;
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
     bool from_before = skey[0] == skey[1];
     for (int i0 = 0; i0 < len; i0 += kAhead) {
-        float v[kAhead][V];
+        uint4 raw[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = i0 + u;
-            const bool on = i < len && skey[i + 1] != dropped;
-            const T* src = dy + static_cast<int64_t>(on ? spos[i] : 0) * a.ldy;
-            if (on && wide) {
-                unpack16(__ldg(reinterpret_cast<const uint4*>(src)), v[u]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < V; ++k) v[u][k] = on && k < nv ? Elem<T>::to_float(src[k]) : 0.f;
-            }
+            raw[u] = make_uint4(0, 0, 0, 0);
+            if (i < len && skey[i + 1] != dropped) raw[u] = load_piece<kWide>(dy + static_cast<int64_t>(spos[i]) * a.ldy, nv);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = i0 + u;
             if (i >= len || skey[i + 1] == dropped) continue;
+            float v[V];
+            unpack16(raw[u], v);
 #pragma unroll
-            for (int k = 0; k < V; ++k) acc[k] += v[u][k];
+            for (int k = 0; k < V; ++k) acc[k] += v[k];
             const bool last = i + 1 == len;
             if (!last && skey[i + 2] == skey[i + 1]) continue;
             const bool goes_on = last && skey[i + 2] == skey[i + 1];
@@ -318,25 +536,32 @@ __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_con
     }
 }
 
-// The block of a chunk whose last run goes on adds that run's partial rows, in order.
+// The block of a chunk whose last run goes on adds that run's partial rows, in
+// order; the run reaches chunk q when q's first key is still its own.
+constexpr int kJoinThreads = 256;
 template <typename T, typename D>
-__global__ void __launch_bounds__(kGradThreads) grad_join_kernel(const __grid_constant__ GradArgs a) {
-    const int64_t chunk = blockIdx.x, next = (chunk + 1) * kChunk;
+__global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const __grid_constant__ GradArgs a) {
+    const int64_t chunk = blockIdx.x, first = chunk * a.chunk, next = first + a.chunk;
     if (next >= a.n) return;
-    const uint32_t key = a.keys[next - 1];
-    if (key == static_cast<uint32_t>(a.vocab) || a.keys[next] != key) return;
-    if (chunk > 0 && a.keys[chunk * kChunk] == key && a.keys[chunk * kChunk - 1] == key) return;   // an earlier chunk's run
-    const int64_t end = lower_bound_key(a.keys, a.n, static_cast<int64_t>(key) + 1);   // one past the run
-    const int64_t last = (end - 1) / kChunk;
-    for (int64_t c = static_cast<int64_t>(blockIdx.y) * kGradThreads + threadIdx.x; c < a.dim;
-         c += static_cast<int64_t>(gridDim.y) * kGradThreads) {
+    const uint32_t key = a.keys[next - 1], after = a.keys[next], head = a.keys[first];
+    const uint32_t before = a.keys[first > 0 ? first - 1 : 0];
+    if (key == static_cast<uint32_t>(a.vocab) || after != key) return;
+    if (first > 0 && head == key && before == key) return;                     // an earlier chunk's run
+    for (int64_t c = static_cast<int64_t>(blockIdx.y) * kJoinThreads + threadIdx.x; c < a.dim;
+         c += static_cast<int64_t>(gridDim.y) * kJoinThreads) {
         float acc = a.part[(chunk * 2 + 1) * a.dim + c];
-        for (int64_t q = chunk + 1; q <= last; q += kAhead) {
+        for (int64_t q = chunk + 1;; q += kAhead) {
             float v[kAhead];
+            bool on[kAhead];
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) v[u] = q + u <= last ? a.part[(q + u) * 2 * a.dim + c] : 0.f;
+            for (int u = 0; u < kAhead; ++u) {
+                on[u] = q + u < a.chunks && a.keys[(q + u) * a.chunk] == key;
+                v[u] = q + u < a.chunks ? a.part[(q + u) * 2 * a.dim + c] : 0.f;   // not a run's: unused
+            }
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) acc += v[u];
+            for (int u = 0; u < kAhead; ++u)
+                if (on[u]) acc += v[u];
+            if (!on[kAhead - 1]) break;
         }
         float one[1] = {acc};
         write_row<D, 1>(a, key, c, 1, one);
@@ -346,7 +571,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_join_kernel(const __grid_co
 struct GradLayout {
     size_t keys[2], pos[2], counts, part, total;
     int64_t chunks;
-    int passes, digit_bits, tiles, rounds;
+    int passes, digit_bits, tiles, rounds, chunk;
 };
 
 GradLayout grad_layout(int64_t n, int64_t vocab, int64_t dim) {
@@ -359,7 +584,9 @@ GradLayout grad_layout(int64_t n, int64_t vocab, int64_t dim) {
     L.rounds = 2;
     while (op_ceil_div(n, static_cast<int64_t>(L.rounds) * kSortThreads) > 128) L.rounds *= 2;
     L.tiles = static_cast<int>(op_ceil_div(n, static_cast<int64_t>(L.rounds) * kSortThreads));
-    L.chunks = op_ceil_div(n, kChunk);
+    L.chunk = kMaxChunk;
+    while (L.chunk > 8 && op_ceil_div(n, L.chunk) * op_ceil_div(dim, kGradThreads * 8) < kGradBlocks) L.chunk /= 2;
+    L.chunks = op_ceil_div(n, L.chunk);
     size_t o = 0;
     auto take = [&](size_t bytes) { const size_t at = o; o = op_align_up(o + bytes, 256); return at; };
     for (int k = 0; k < 2; ++k) L.keys[k] = take(static_cast<size_t>(n) * 4);
@@ -374,20 +601,26 @@ template <typename T, typename D>
 cudaError_t launch_grad(const GradArgs& a0, cudaStream_t s) {
     GradArgs a = a0;
     constexpr int V = Elem<T>::kVec;
-    a.wide_in = op_aligned(a.dy, 16) && (a.ldy * sizeof(T)) % 16 == 0;
+    const bool wide_in = op_aligned(a.dy, 16) && (a.ldy * sizeof(T)) % 16 == 0;
     a.wide_out = op_aligned(a.dw, 16) && (a.ldw * sizeof(D)) % 16 == 0;
     const int64_t slabs = op_ceil_div(a.dim, static_cast<int64_t>(kGradThreads) * V);
     a.sum_blocks = a.chunks * slabs;
-    const int64_t zero_blocks = a.accumulate ? 0 : op_ceil_div(a.vocab, kZeroRows);
+    a.zero_rows = kMaxZeroRows;
+    while (a.zero_rows > 4 && op_ceil_div(a.vocab, a.zero_rows) < 4 * kGradBlocks) a.zero_rows /= 2;
+    const int64_t zero_blocks = a.accumulate ? 0 : op_ceil_div(a.vocab, a.zero_rows);
     if (a.sum_blocks + zero_blocks > 0) {
-        grad_sum_kernel<T, D><<<static_cast<unsigned>(a.sum_blocks + zero_blocks), kGradThreads, 0, s>>>(a);
+        const unsigned grid = static_cast<unsigned>(a.sum_blocks + zero_blocks);
+        if (wide_in)
+            grad_sum_kernel<T, D, true><<<grid, kGradThreads, 0, s>>>(a);
+        else
+            grad_sum_kernel<T, D, false><<<grid, kGradThreads, 0, s>>>(a);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     if (a.chunks > 1) {
-        const int64_t by = op_ceil_div(a.dim, kGradThreads);
+        const int64_t by = op_ceil_div(a.dim, 2 * kJoinThreads);
         grad_join_kernel<T, D><<<dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(by < 64 ? by : 64)),
-                                 kGradThreads, 0, s>>>(a);
+                                 kJoinThreads, 0, s>>>(a);
         return cudaGetLastError();
     }
     return cudaSuccess;
@@ -429,8 +662,8 @@ int embedding_lookup(const void* W, int w_dtype, int64_t vocab, int64_t dim, int
 int embedding_grad_workspace_bytes(int64_t n, int64_t vocab, int64_t dim, size_t* bytes_out) {
     if (n < 0 || vocab < 0 || dim < 0 || bytes_out == nullptr) return MO_ERR_INVALID_ARG;
     if (vocab >= kMaxCount || n > kMaxCount || dim > kMaxDim) return MO_ERR_UNSUPPORTED;
-    // one block for each chunk and column slab, and for each kZeroRows rows: a grid's limit
-    if (op_ceil_div(n, kChunk) * op_ceil_div(dim, kGradThreads * 4) + op_ceil_div(vocab, kZeroRows) > kMaxCount)
+    // one block for each chunk and column slab, and for each block of zeroed rows: a grid's limit
+    if (op_ceil_div(n, kMaxChunk) * op_ceil_div(dim, kGradThreads * 4) + op_ceil_div(vocab, kMaxZeroRows) > kMaxCount)
         return MO_ERR_UNSUPPORTED;
     *bytes_out = grad_layout(n, vocab, dim).total;
     return MO_OK;
@@ -459,6 +692,8 @@ int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t
     uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(base + L.pos[0]), reinterpret_cast<uint32_t*>(base + L.pos[1])};
     if (n > 0) {
         const cudaError_t e = op_traced(MO_K_EMBED_SORT, s, [&] {
+            if (n <= kClusterSortMax && vocab <= kClusterVocabMax)
+                return launch_cluster_sort<1>(ids, id_dtype, n, vocab, keys[(L.passes + 1) & 1], pos[(L.passes + 1) & 1], s);
             for (int k = 0; k < L.passes; ++k) {
                 SortPass p;
                 p.ids = ids;
@@ -471,6 +706,7 @@ int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t
                 p.n = n;
                 p.vocab = vocab;
                 p.shift = k * L.digit_bits;
+                p.digit_bits = L.digit_bits;
                 p.digits = 1 << L.digit_bits;
                 p.tiles = L.tiles;
                 p.rounds = L.rounds;
@@ -497,6 +733,7 @@ int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t
     a.part = reinterpret_cast<float*>(base + L.part);
     a.scale = scale;
     a.accumulate = accumulate;
+    a.chunk = L.chunk;
     a.chunks = L.chunks;
     return op_status(op_traced(MO_K_EMBED_GRAD, s, [&] {
         if (dy_dtype == MO_F32) return dw_dtype == MO_F32 ? launch_grad<float, float>(a, s) : launch_grad<float, bf16>(a, s);

@@ -15,9 +15,9 @@ def embedding_lookup(W, ids, scale=1.0):
 def embedding_grad(dY, ids, vocab, scale=1.0, start=None):
     dY = np.asarray(dY, np.float64)
     out = np.zeros((vocab, dY.shape[1])) if start is None else np.array(start, np.float64)
-    for i, v in enumerate(np.asarray(ids)):
-        if 0 <= v < vocab:
-            out[v] += scale * dY[i]
+    ids = np.asarray(ids)
+    keep = (ids >= 0) & (ids < vocab)
+    np.add.at(out, ids[keep], scale * dY[keep])
     return out
 
 

@@ -75,7 +75,8 @@ GRAD_CASES = [
     (1, 1, 1, None, 0, "one"), (5, 3, 8, None, 0, "uniform"), (64, 1000, 64, None, 0, "uniform"),
     (777, 503, 515, None, 0, "zipf"), (129, 40, 95, 99, 3, "uniform"), (300, 700, 128, 136, 0, "zipf"),
     (3000, 257, 72, None, 0, "one"), (5000, 2000, 1032, None, 0, "zipf"), (1025, 512, 16, None, 0, "sorted"),
-    (700, 511, 24, None, 0, "dropped"), (20000, 300000, 8, None, 0, "uniform")]
+    (700, 511, 24, None, 0, "dropped"), (20000, 300000, 8, None, 0, "uniform"),
+    (65536, 1023, 4, None, 0, "zipf"), (70001, 1500, 4, None, 0, "zipf"), (140001, 1500, 4, None, 0, "zipf"), (8193, 600, 12, None, 0, "one")]
 
 
 def _ids(rng, n, vocab, how):

@@ -130,5 +130,3 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         with pytest.raises(B.MoError) as e:
             call()
         assert e.value.status == B.MO_ERR_INVALID_ARG
-    with pytest.raises(B.MoError):
-        B.id_dtype_code(torch.int16)
