@@ -66,8 +66,8 @@ struct Ctl {
     uint64_t tail[kMaxStages], tail_peer[kMaxStages];     // pair, wgrad: a sum's ragged last block in that stage
     uint32_t tmem_base;
     int abort_flag;
-    int64_t cum[kMaxExperts + 1];                         // token tiles before expert e
-    int32_t row[kMaxExperts + 1];                         // first row of expert e, held inside [0, rows]
+    int32_t cum[kMaxExperts + 1];                         // token tiles before expert e
+    int32_t row[kMaxExperts + 1];                         // first row of expert e: not falling, inside [0, rows]
 };
 constexpr int kCtlBytes = (sizeof(Ctl) + 1023) / 1024 * 1024;
 constexpr int kSmemBytes = kRingBytes + kEpiWarps * kOutBytes + kCtlBytes + 1024;
@@ -82,6 +82,9 @@ struct ExpertArgs {
     int64_t ldo, stride_o;
     int32_t rows, n, k, experts;
     int32_t out_f32, accumulate;
+    int32_t f_tiles;               // tiles over the output features
+    int32_t width, c_tiles;        // wgrad: columns of a tile, tiles over the k columns
+    int32_t splits;                // parts of every sum, each into an output of its own (joined afterwards)
     int32_t chunk;                 // K blocks summed in TMEM before the float32 sum moves on to registers
     int* err;
 };
@@ -92,6 +95,8 @@ struct Tile {
     int c0, cn;                    // first column (absolute token row, or k) and how many are real
     int nmma;                      // columns of the MMA: cn rounded up to 16 (pair: 32)
     int r0, depth;                 // wgrad: first row of the sum; length of the sum
+    int kb0, kb1;                  // the K blocks (of kBK) of this tile's part of the sum
+    int split;
 };
 
 // tcgen05 instruction descriptor: bf16 x bf16 -> f32, M x N.
@@ -101,11 +106,10 @@ __device__ __forceinline__ uint32_t instr_desc(uint32_t m, uint32_t n, uint32_t 
 
 __device__ __forceinline__ int ceil_div_i(int a, int b) { return (a + b - 1) / b; }
 
-template <int kMode, bool kPair>
-__device__ __forceinline__ int64_t tile_count(const ExpertArgs& p, const Ctl* ctl) {
-    if (kMode == kWgrad)
-        return static_cast<int64_t>(p.experts) * ceil_div_i(p.n, Geo<kPair>::kFeatures) * ceil_div_i(p.k, kBN);
-    return ctl->cum[p.experts] * ceil_div_i(kMode == kFwd ? p.n : p.k, Geo<kPair>::kFeatures);
+// (the host sees to it that tile numbers fit 31 bits)
+template <int kMode>
+__device__ __forceinline__ int tile_count(const ExpertArgs& p, const Ctl* ctl) {
+    return (kMode == kWgrad ? p.experts * p.c_tiles : ctl->cum[p.experts]) * p.f_tiles * p.splits;
 }
 
 // Tile u of the walk.  Forward and dgrad go expert by expert, within one in
@@ -113,42 +117,52 @@ __device__ __forceinline__ int64_t tile_count(const ExpertArgs& p, const Ctl* ct
 // tokens innermost: the CTAs at work together then share a few thousand tokens
 // and features, which stay in L2.
 template <int kMode, bool kPair>
-__device__ __forceinline__ Tile tile_at(const ExpertArgs& p, const Ctl* ctl, int64_t u) {
+__device__ __forceinline__ Tile tile_at(const ExpertArgs& p, const Ctl* ctl, int tile) {
     using G = Geo<kPair>;
     Tile t;
+    uint32_t u = static_cast<uint32_t>(tile);
+    t.split = 0;
+    if (p.splits > 1) {
+        t.split = static_cast<int>(u % p.splits);
+        u /= p.splits;
+    }
     if (kMode == kWgrad) {
-        const int tk = ceil_div_i(p.k, kBN), per = ceil_div_i(p.n, G::kFeatures) * tk;
-        t.e = static_cast<int>(u / per);
-        const int v = static_cast<int>(u - static_cast<int64_t>(t.e) * per);
-        t.f0 = v / tk * G::kFeatures;
-        t.c0 = v % tk * kBN;
-        t.cn = min(kBN, p.k - t.c0);
+        const uint32_t strip = u / p.c_tiles, c = u - strip * p.c_tiles;       // strip: one expert's feature tile
+        t.e = static_cast<int>(strip / p.f_tiles);
+        t.f0 = static_cast<int>(strip - t.e * p.f_tiles) * G::kFeatures;
+        t.c0 = static_cast<int>(c) * p.width;
+        t.cn = min(p.width, p.k - t.c0);
         t.r0 = ctl->row[t.e];
-        t.depth = max(0, ctl->row[t.e + 1] - t.r0);
+        t.depth = ctl->row[t.e + 1] - t.r0;
     } else {
-        const int tf = ceil_div_i(kMode == kFwd ? p.n : p.k, G::kFeatures);
+        const int strip = static_cast<int>(u / p.f_tiles);                     // counts token tiles of the experts before
         int lo = 0, hi = p.experts - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (ctl->cum[mid] * tf <= u) lo = mid; else hi = mid - 1;
+            if (ctl->cum[mid] <= strip) lo = mid; else hi = mid - 1;
         }
         t.e = lo;
-        const int64_t v = u - ctl->cum[lo] * tf;
-        const int nt = static_cast<int>(ctl->cum[lo + 1] - ctl->cum[lo]);
-        const int64_t per = static_cast<int64_t>(kTokenGroup) * tf;
+        const int nt = ctl->cum[lo + 1] - ctl->cum[lo];
+        const uint32_t v = u - static_cast<uint32_t>(ctl->cum[lo]) * p.f_tiles, per = kTokenGroup * p.f_tiles;
         const int g = static_cast<int>(v / per);
-        const int w = static_cast<int>(v - g * per);
-        const int gs = min(kTokenGroup, nt - g * kTokenGroup);
-        const int tok = g * kTokenGroup + w % gs;
-        const int m = ctl->row[lo + 1] - ctl->row[lo];
-        const int size = (ceil_div_i(m, nt) + 15) / 16 * 16;      // equal tiles, at most kBN tokens
-        t.f0 = w / gs * G::kFeatures;
+        const uint32_t w = v - g * per, gs = min(kTokenGroup, nt - g * kTokenGroup);
+        const int m = ctl->row[lo + 1] - ctl->row[lo], f = static_cast<int>(w / gs);
+        const int tok = g * kTokenGroup + static_cast<int>(w - f * gs);
+        const int size = (ceil_div_i(m, nt) + 15) / 16 * 16;                   // equal tiles, at most kBN tokens
+        t.f0 = f * G::kFeatures;
         t.c0 = ctl->row[lo] + tok * size;
         t.cn = min(size, m - tok * size);
         t.r0 = 0;
         t.depth = kMode == kFwd ? p.k : p.n;
     }
     t.nmma = (t.cn + G::kRound - 1) / G::kRound * G::kRound;
+    t.kb0 = 0;
+    t.kb1 = ceil_div_i(t.depth, kBK);
+    if (p.splits > 1) {
+        const int part = ceil_div_i(t.kb1, p.splits);
+        t.kb0 = min(t.split * part, t.kb1);
+        t.kb1 = min(t.kb0 + part, t.kb1);
+    }
     return t;
 }
 
@@ -249,8 +263,8 @@ __device__ __forceinline__ void zero_tail(uint32_t stage, int boxes, int v, int 
 // in whole 16-byte pieces (measured: it wrote the elements between the end and
 // the next 16-byte boundary), so a block with an end inside a piece is stored plainly.
 template <bool kF32>
-__device__ __forceinline__ void put_tokens(const ExpertArgs& p, int cols, int f, int token, int valid, const float* v,
-                                           uint32_t buf, int lane) {
+__device__ __forceinline__ void put_tokens(const ExpertArgs& p, int cols, int f, int64_t token, int valid,
+                                           const float* v, uint32_t buf, int lane) {
     constexpr int kTok = kF32 ? 16 : 32;               // tokens of one 2 KB block
     constexpr int kRow = kF32 ? 128 : 64;              // bytes of one token's 32 features
     const bool whole = f + 32 <= cols || cols % (kF32 ? 4 : 8) == 0;
@@ -271,7 +285,7 @@ __device__ __forceinline__ void put_tokens(const ExpertArgs& p, int cols, int f,
         __syncwarp();
         if (nv == kTok && whole) {
             if (elect_one()) {
-                tma_store_2d(&p.o, buf, f, token + h * kTok);
+                tma_store_2d(&p.o, buf, f, static_cast<int>(token + h * kTok));
                 bulk_commit();
             }
         } else {
@@ -279,7 +293,7 @@ __device__ __forceinline__ void put_tokens(const ExpertArgs& p, int cols, int f,
             for (int j = lane; j < nv * kPieces; j += 32) {
                 const int t = j / kPieces, q = j % kPieces, c = f + q * kPer;
                 if (c >= cols) continue;
-                const int64_t at = static_cast<int64_t>(token + h * kTok + t) * p.ldo + c;
+                const int64_t at = (token + h * kTok + t) * p.ldo + c;
                 const uint32_t src = buf + t * kRow + q * 16;
                 if (c + kPer <= cols) {
                     void* dst = kF32 ? static_cast<void*>(static_cast<float*>(p.out) + at)
@@ -408,24 +422,32 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         }
     }
     if (warp == 0) {                                   // the experts' rows and token tiles
-        int64_t carry = 0;
+        int carry = 0, top = 0;
         if (lane == 0) ctl->cum[0] = 0;
         for (int base = 0; base <= p.experts; base += 32) {
             const int e = base + lane;
-            int a = 0, b = 0;
-            if (e <= p.experts) {
-                a = min(max(p.offsets[e], 0), p.rows);
-                ctl->row[e] = a;
+            int a = e <= p.experts ? min(max(p.offsets[e], 0), p.rows) : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {                              // never below an earlier one
+                const int up = __shfl_up_sync(0xffffffffu, a, o);
+                if (lane >= o) a = max(a, up);
             }
-            if (e < p.experts) b = min(max(p.offsets[e + 1], 0), p.rows);
-            int64_t tiles = e < p.experts && b > a ? (b - a + kBN - 1) / kBN : 0;
+            a = max(a, top);
+            // the expert before ends where this one begins
+            int before = __shfl_up_sync(0xffffffffu, a, 1);
+            if (lane == 0) before = top;
+            int tiles = e > 0 && e <= p.experts ? (a - before + kBN - 1) / kBN : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(0xffffffffu, tiles, o);
+                const int up = __shfl_up_sync(0xffffffffu, tiles, o);
                 if (lane >= o) tiles += up;
             }
-            if (e < p.experts) ctl->cum[e + 1] = carry + tiles;
+            if (e <= p.experts) {
+                ctl->row[e] = a;
+                ctl->cum[e] = carry + tiles;                                // of the experts before e
+            }
             carry += __shfl_sync(0xffffffffu, tiles, 31);
+            top = __shfl_sync(0xffffffffu, a, 31);
         }
     }
     tc_fence_before();
@@ -434,22 +456,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = ctl->tmem_base;
     volatile int* abort_flag = &ctl->abort_flag;
-    const int64_t tiles = tile_count<kMode, kPair>(p, ctl);
+    const int tiles = tile_count<kMode>(p, ctl);
 
     if (warp == kProducerWarp) {
         int stage = 0;
         uint32_t phase = 0, narmed = 0;
         uint32_t tail_used = 0, tail_phase = 0;         // by stage: ragged last blocks armed, the parity of the last
         bool ok = true;
-        for (int64_t u = unit; u < tiles && ok; u += units) {
+        for (int u = unit; u < tiles && ok; u += units) {
             const Tile t = tile_at<kMode, kPair>(p, ctl, u);
-            const int nkb = ceil_div_i(t.depth, kBK);
             // this CTA's features and columns
             const int f0 = t.f0 + static_cast<int>(rank) * kBM;
             const int mine = t.nmma / G::kCtas, c0 = t.c0 + static_cast<int>(rank) * mine;
             const int nb = (mine + 63) / 64;                         // wgrad: 64-wide boxes of X
             const uint32_t bytes = kABytes + (kMode == kWgrad ? nb * 8192 : mine * kBK * 2);
-            for (int kb = 0; kb < nkb; ++kb) {
+            for (int kb = t.kb0; kb < t.kb1; ++kb) {
                 if (!warp_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err, 0x201)) {
                     ok = false;
                     break;
@@ -458,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 // gradient's ragged last block counts on each CTA's own, because each
                 // zeroes its part before the leader may use it; the stage's full barrier
                 // then only turns its phase over.
-                const bool tail = kPair && kMode == kWgrad && kb + 1 == nkb && t.depth % kBK != 0;
+                const bool tail = kPair && kMode == kWgrad && (kb + 1) * kBK > t.depth;
                 if (tail) {
                     tail_phase ^= (tail_used >> stage & 1u) << stage;
                     tail_used |= 1u << stage;
@@ -537,9 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         uint32_t phase = 0, tail_phase = 0;             // tail_phase: by stage
         bool ok = true;
         int q = 0;                                      // chunks so far: accumulator ping-pong
-        for (int64_t u = unit; u < tiles && ok; u += units) {
+        for (int u = unit; u < tiles && ok; u += units) {
             const Tile t = tile_at<kMode, kPair>(p, ctl, u);
-            const int nkb = ceil_div_i(t.depth, kBK);
             const uint32_t idesc = instr_desc(G::kFeatures, t.nmma, kMode != kFwd, kMode == kWgrad);
             // K-major operands: 8-row groups 1 KB apart, 32 bytes per 16-wide step.
             // MN-major operands: 64-column blocks 8 KB apart, 8-row K groups 1 KB
@@ -548,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             const uint64_t bd0 = kMode == kWgrad ? sdesc_sw128(0, 8192, 1024) : sdesc_sw128(0, 16, 1024);
             constexpr uint32_t a_step = (kMode == kFwd ? 32 : 2048) >> 4, b_step = (kMode == kWgrad ? 2048 : 32) >> 4;
             int in_chunk = 0;
-            for (int kb = 0; kb < nkb; ++kb) {
+            for (int kb = t.kb0; kb < t.kb1; ++kb) {
                 if (in_chunk == 0 &&
                     !warp_wait(smem_u32(&ctl->tempty[q & 1]), ((q >> 1) & 1) ^ 1u, abort_flag, p.err, 0x202)) {
                     ok = false;
@@ -560,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 }
                 const uint32_t sa = smem_u32(smem + stage * G::kStageBytes), sb = sa + kABytes;
                 int steps = kBK / 16;
-                if (kMode == kWgrad && kb + 1 == nkb && t.depth % kBK != 0) {   // the sum ends inside this block
+                if (kMode == kWgrad && (kb + 1) * kBK > t.depth) {              // the sum ends inside this block
                     const int v = t.depth - kb * kBK, boxes = 2 + (t.nmma / G::kCtas + 63) / 64;
                     steps = (v + 15) / 16;
                     if (kPair && !warp_wait(smem_u32(&ctl->tail[stage]), tail_phase >> stage & 1u, abort_flag, p.err, 0x205)) {
@@ -595,11 +615,11 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                         for (int k = 0; k < steps; ++k) mma(k);
                     }
                     commit<kPair>(smem_u32(&ctl->empty[stage]));
-                    if (in_chunk + 1 == p.chunk || kb + 1 == nkb) commit<kPair>(smem_u32(&ctl->tfull[q & 1]));
+                    if (in_chunk + 1 == p.chunk || kb + 1 == t.kb1) commit<kPair>(smem_u32(&ctl->tfull[q & 1]));
                 }
                 __syncwarp();
                 if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-                if (++in_chunk == p.chunk || kb + 1 == nkb) {
+                if (++in_chunk == p.chunk || kb + 1 == t.kb1) {
                     ++q;
                     in_chunk = 0;
                 }
@@ -615,10 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         if (kMode == kWgrad) {
             uint32_t tail_phase = 0;                    // by stage
             int64_t blocks = 0;                         // K blocks so far: the ring's position
-            for (int64_t u = unit; u < tiles; u += units) {
+            for (int u = unit; u < tiles; u += units) {
                 const Tile t = tile_at<kMode, kPair>(p, ctl, u);
-                blocks += ceil_div_i(t.depth, kBK);
-                if (t.depth % kBK == 0) continue;
+                blocks += t.kb1 - t.kb0;
+                if (t.kb1 == t.kb0 || t.kb1 * kBK <= t.depth) continue;
                 const int stage = static_cast<int>((blocks - 1) % G::kStages);
                 bool there = true;
                 if (lane == 0)
@@ -637,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     } else {
         const int quarter = warp & 3, half = warp >> 2;
         const uint32_t buf = smem_u32(smem + kRingBytes + warp * kOutBytes);
-        if (kMode != kWgrad) {                          // rows of no expert
+        if (kMode != kWgrad && p.splits == 1) {         // rows of no expert
             const int head = ctl->row[0], tail = ctl->row[p.experts];
             const int64_t extra = static_cast<int64_t>(head) + (p.rows - tail);
             for (int64_t r = blockIdx.x * kEpiWarps + warp; r < extra; r += static_cast<int64_t>(gridDim.x) * kEpiWarps) {
@@ -654,9 +674,13 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                                            kPair ? mapa_shared(smem_u32(&ctl->tempty[1]), 0) : 0u};
         bool ok = true;
         int q = 0;
-        for (int64_t u = unit; u < tiles && ok; u += units) {
-            const Tile t = tile_at<kMode, kPair>(p, ctl, u);
-            const int nkb = ceil_div_i(t.depth, kBK), chunks = ceil_div_i(nkb, p.chunk);
+        for (int u = unit; u < tiles && ok; u += units) {
+            int chunks, nmma;
+            {
+                const Tile t = tile_at<kMode, kPair>(p, ctl, u);
+                chunks = ceil_div_i(t.kb1 - t.kb0, p.chunk);
+                nmma = t.nmma;
+            }
             float v[4][32];                             // this lane's row of the warp's 32-column groups
 #pragma unroll
             for (int g = 0; g < 4; ++g)
@@ -669,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
                     const int col = (2 * g + half) * 32;
-                    if (col >= t.nmma) continue;        // warp-uniform
+                    if (col >= nmma) continue;          // warp-uniform
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                            static_cast<uint32_t>((q & 1) * kBN + col), r);
@@ -687,6 +711,9 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 }
             }
             if (!ok) break;
+            int again = u;                              // the tile's place once more: holding it over the sums spills registers
+            asm volatile("" : "+r"(again));
+            const Tile t = tile_at<kMode, kPair>(p, ctl, again);
             if (kMode == kWgrad && t.depth == 0 && p.accumulate) continue;
             const int f = t.f0 + static_cast<int>(rank) * kBM + quarter * 32;
             if (f >= (kMode == kWgrad ? p.n : cols)) continue;
@@ -695,9 +722,10 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 const int col = (2 * g + half) * 32;
                 if (col >= t.cn) continue;
                 if (kMode == kWgrad)
-                    put_weights<kF32>(p, t.e, f, t.c0 + col, v[g], buf, lane);
+                    put_weights<kF32>(p, t.split * p.experts + t.e, f, t.c0 + col, v[g], buf, lane);
                 else
-                    put_tokens<kF32>(p, cols, f, t.c0 + col, min(32, t.cn - col), v[g], buf, lane);
+                    put_tokens<kF32>(p, cols, f, static_cast<int64_t>(t.split) * p.rows + t.c0 + col, min(32, t.cn - col),
+                                     v[g], buf, lane);
             }
         }
         if (elect_one()) bulk_wait_all();               // no store still reads this CTA's shared memory
@@ -726,6 +754,57 @@ __global__ void __launch_bounds__(256) fill_zero_kernel(void* out, int out_f32, 
             static_cast<float*>(out)[at] = 0.f;
         else
             static_cast<bf16*>(out)[at] = __float2bfloat16_rn(0.f);
+    }
+}
+
+// Adds the parts of split sums in order: out (+)= sum_s part[s], four columns per
+// thread.  Rows of no expert (forward, dgrad: row0 .. row1 hold the experts') are zeros.
+struct JoinArgs {
+    const float* part;             // [splits][rows][ld]
+    void* out;
+    const int32_t* offsets;        // null for a weight gradient
+    int64_t rows, cols, ld, ldo, stride_o, matrix_rows;
+    int32_t splits, out_f32, accumulate, experts;
+};
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs p) {
+    const int64_t groups = p.ld / 4, total = p.rows * groups;
+    int64_t r0 = 0, r1 = p.rows;
+    if (p.offsets != nullptr) {
+        r0 = min(max(static_cast<int64_t>(p.offsets[0]), int64_t(0)), p.rows);
+        r1 = min(max(static_cast<int64_t>(p.offsets[p.experts]), int64_t(0)), p.rows);
+    }
+    for (int64_t i = blockIdx.x * 256LL + threadIdx.x; i < total; i += 256LL * gridDim.x) {
+        const int64_t r = i / groups, c = (i - r * groups) * 4, e = r / p.matrix_rows;
+        const int64_t at = e * p.stride_o + (r - e * p.matrix_rows) * p.ldo + c;
+        const int nv = static_cast<int>(min(p.cols - c, int64_t(4)));
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r >= r0 && r < r1)
+            for (int s = 0; s < p.splits; ++s) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(p.part + (s * p.rows + r) * p.ld + c));
+                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+            }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k >= nv) continue;
+            if (p.accumulate)
+                v[k] += p.out_f32 ? static_cast<const float*>(p.out)[at + k]
+                                  : __bfloat162float(static_cast<const bf16*>(p.out)[at + k]);
+        }
+        if (nv == 4) {                                  // rows start on 16-byte boundaries
+            if (p.out_f32)
+                store_run<float, 4>(static_cast<float*>(p.out) + at, v, true);
+            else
+                store_run<bf16, 4>(static_cast<bf16*>(p.out) + at, v, true);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (k >= nv) continue;
+                if (p.out_f32)
+                    static_cast<float*>(p.out)[at + k] = v[k];
+                else
+                    static_cast<bf16*>(p.out)[at + k] = __float2bfloat16_rn(v[k]);
+            }
+        }
     }
 }
 
@@ -852,7 +931,63 @@ constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
 constexpr int64_t kMaxSide = int64_t(1) << 20;
 constexpr size_t kExpertHeader = 256;      // the error word that mo_check_device_status reads
 
-size_t expert_ws_bytes() { return kExpertHeader; }
+// How a call runs: on CTA pairs or single CTAs, and in how many parts each sum.
+struct Plan {
+    bool pair;
+    int splits;
+};
+
+// Tiles of a call at most (each expert may end in a tile of its own).
+int64_t most_tiles(int mode, int64_t rows, int64_t n, int64_t k, int experts, bool pair) {
+    const int64_t features = pair ? 2 * kBM : kBM;
+    if (mode == kWgrad) return experts * op_ceil_div(n, features) * op_ceil_div(k, kBN);
+    return (rows / kBN + std::min<int64_t>(experts, rows)) * op_ceil_div(mode == kFwd ? n : k, features);
+}
+
+constexpr int64_t kSms = 152;
+constexpr int64_t kShortSum = 512;         // rows per expert from which a weight gradient runs on pairs
+constexpr int64_t kSplitBlocks = 24;       // K blocks that a split has to take off a tile's time
+constexpr int64_t kMinSplitBlocks = 4;     // K blocks of a part, at least
+
+// Pairs halve the operand bytes per SM; a weight gradient over few rows is bound by
+// its stores instead, which single CTAs (more of them, each waiting for itself alone)
+// issue faster.  Measured (us, single / pair): forward of 16384 rows, 8 experts of
+// 4096 x 4096 334 / 296; 64 rows, 8 experts of 4096 x 4096 49 / 46; 16 rows, 16 experts of
+// 2048 x 1024 8.1 / 8.9; float32 weight gradient over 1024 rows each, 16 experts of 2048 x
+// 2048 138 / 126; over 512 (32 of 1024 x 1024) 50.7 / 51.9; over 256 (16 of 2048 x 2048) 69 / 75.
+// Where the tiles leave at least half of the SMs idle and the sums are long, each sum is
+// split into parts that are joined in order afterwards (about 3 us more).
+Plan plan_call(int mode, int64_t rows, int64_t n, int64_t k, int experts, int forced) {
+    const int64_t depth = mode == kFwd ? k : mode == kDgrad ? n : op_ceil_div(rows, experts);
+    const int64_t blocks = op_ceil_div(depth, kBK);
+    Plan p;
+    p.pair = mode == kWgrad ? depth >= kShortSum
+                            : depth > 1024 || most_tiles(mode, rows, n, k, experts, true) > 2 * (kSms / 2);
+    if (forced >= 0) p.pair = forced == 1;
+    const int64_t tiles = most_tiles(mode, rows, n, k, experts, p.pair), units = p.pair ? kSms / 2 : kSms;
+    p.splits = 1;
+    if (tiles > 0 && 2 * tiles <= units) {
+        const int64_t s = std::min(units / tiles, blocks / kMinSplitBlocks);
+        if (s >= 2 && blocks - op_ceil_div(blocks, s) >= kSplitBlocks) p.splits = static_cast<int>(s);
+    }
+    return p;
+}
+
+// Rows and row pitch of one part of a split call's output.
+int64_t part_rows(int mode, int64_t rows, int64_t n, int experts) { return mode == kWgrad ? experts * n : rows; }
+int64_t part_ld(int mode, int64_t n, int64_t k) { return op_ceil_div(mode == kFwd ? n : k, 4) * 4; }
+
+size_t expert_ws_bytes(int64_t rows, int64_t n, int64_t k, int experts) {
+    size_t most = 0;
+    for (int mode = kFwd; mode <= kWgrad; ++mode)
+        for (int forced = 0; forced < 2; ++forced) {
+            const Plan p = plan_call(mode, rows, n, k, experts, forced);
+            if (p.splits > 1)
+                most = std::max(most, static_cast<size_t>(p.splits) * static_cast<size_t>(part_rows(mode, rows, n, experts)) *
+                                          static_cast<size_t>(part_ld(mode, n, k)) * 4);
+        }
+    return kExpertHeader + op_align_up(most, 256);
+}
 
 int check_sizes(int64_t rows, int64_t n, int64_t k, int experts) {
     if (rows < 0 || n < 0 || k < 0 || experts < 1) return MO_ERR_INVALID_ARG;
@@ -876,10 +1011,9 @@ int check_stack(int dt, int64_t rows, int64_t ld, int64_t stride, int experts) {
 int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_t stream) {
     if (q.offsets == nullptr) return MO_ERR_INVALID_ARG;
     if (!op_aligned(q.offsets, 4)) return MO_ERR_ALIGNMENT;
-    const int st = op_check_ws(ws, ws_bytes, expert_ws_bytes());
+    const int st = op_check_ws(ws, ws_bytes, expert_ws_bytes(q.rows, q.n, q.k, q.experts));
     if (st != MO_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool f32 = q.out_dtype == MO_F32;
     const int64_t cols = mode == kFwd ? q.n : q.k;      // of the output
     const int64_t depth = mode == kFwd ? q.k : mode == kDgrad ? q.n : q.rows;
     if (depth == 0) {
@@ -887,48 +1021,75 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
         const int64_t rows = mode == kWgrad ? q.n : q.rows, total = rows * cols * (mode == kWgrad ? q.experts : 1);
         return op_status(op_traced(MO_K_EXPERT + mode, s, [&] {
             fill_zero_kernel<<<static_cast<unsigned>(std::min<int64_t>(op_ceil_div(total, 256), 16384)), 256, 0, s>>>(
-                q.out, f32, rows, cols, q.ldo, q.stride_o, total);
+                q.out, q.out_dtype == MO_F32, rows, cols, q.ldo, q.stride_o, total);
             return cudaGetLastError();
         }));
     }
     if (!get_encode()) return MO_ERR_CUDA;
-    const int forced = g_expert_pair.load();
-    const bool pair = forced >= 0 ? forced == 1 : true;
-    const int features = pair ? 2 * kBM : kBM;
+    const Plan plan = plan_call(mode, q.rows, q.n, q.k, q.experts, g_expert_pair.load());
+    const bool split = plan.splits > 1;
+    const bool f32 = split || q.out_dtype == MO_F32;    // of what the product kernel writes
+    float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kExpertHeader);
+    const int64_t rows_part = part_rows(mode, q.rows, q.n, q.experts), ld_part = part_ld(mode, q.n, q.k);
+    void* out = split ? parts : q.out;
+    const int out_dtype = f32 ? MO_F32 : MO_BF16;
+    const int64_t ldo = split ? ld_part : q.ldo, stride_o = split ? q.n * ld_part : q.stride_o;
     ExpertArgs p;
+    const int64_t features = plan.pair ? 2 * kBM : kBM, tk = op_ceil_div(q.k, kBN);
+    p.f_tiles = static_cast<int32_t>(op_ceil_div(mode == kWgrad ? q.n : cols, features));
+    p.width = static_cast<int32_t>(op_ceil_div(op_ceil_div(q.k, tk), 32) * 32);     // equal tiles of at most kBN columns
+    p.c_tiles = static_cast<int32_t>(op_ceil_div(q.k, p.width));
+    const int64_t tiles = most_tiles(mode, q.rows, q.n, q.k, q.experts, plan.pair) * plan.splits;
+    if (tiles > INT32_MAX) return MO_ERR_UNSUPPORTED;
     bool ok;
-    int64_t most_tiles;
     constexpr auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
     if (mode == kWgrad) {
         ok = encode(&p.a, q.a, MO_BF16, q.n, q.rows, 1, q.lda, 0, 2, 64, 64, k128) &&
              encode(&p.b[0], q.b, MO_BF16, q.k, q.rows, 1, q.ldb, 0, 2, 64, 64, k128) &&
-             encode(&p.o, q.out, q.out_dtype, q.k, q.n, q.experts, q.ldo, q.stride_o, 3, f32 ? 16 : 32, 32,
-                    CU_TENSOR_MAP_SWIZZLE_64B);
+             encode(&p.o, out, out_dtype, q.k, q.n, static_cast<int64_t>(q.experts) * plan.splits, ldo, stride_o, 3,
+                    f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
         for (int i = 1; i < kBoxes; ++i) p.b[i] = p.b[0];
-        most_tiles = q.experts * op_ceil_div(q.n, features) * op_ceil_div(q.k, kBN);
     } else {
         ok = encode(&p.a, q.b, MO_BF16, q.k, q.n, q.experts, q.ldb, q.stride_b, 3, 64, mode == kFwd ? 128 : 64, k128) &&
-             encode(&p.o, q.out, q.out_dtype, cols, q.rows, 1, q.ldo, 0, 2, 32, f32 ? 16 : 32, CU_TENSOR_MAP_SWIZZLE_NONE);
+             encode(&p.o, out, out_dtype, cols, q.rows * plan.splits, 1, ldo, 0, 2, 32, f32 ? 16 : 32,
+                    CU_TENSOR_MAP_SWIZZLE_NONE);
         for (int i = 0; i < kBoxes; ++i)
             ok = ok && encode(&p.b[i], q.a, MO_BF16, depth, q.rows, 1, q.lda, 0, 2, 64, 128 >> i, k128);
-        // each expert may end in a tile of its own
-        most_tiles = (q.rows / kBN + std::min<int64_t>(q.experts, q.rows)) * op_ceil_div(cols, features);
     }
     if (!ok) return MO_ERR_UNSUPPORTED;                 // a stride past what a tensor map holds (2^40 bytes)
     p.offsets = q.offsets;
-    p.out = q.out;
-    p.ldo = q.ldo;
-    p.stride_o = q.stride_o;
+    p.out = out;
+    p.ldo = ldo;
+    p.stride_o = stride_o;
     p.rows = static_cast<int32_t>(q.rows);
     p.n = static_cast<int32_t>(q.n);
     p.k = static_cast<int32_t>(q.k);
     p.experts = q.experts;
     p.out_f32 = f32;
-    p.accumulate = q.accumulate;
+    p.accumulate = split ? 0 : q.accumulate;
+    p.splits = plan.splits;
     p.chunk = f32 ? kF32Chunk : 1 << 26;                 // more blocks than any sum has
     p.err = static_cast<int*>(ws);
     return op_status(op_traced(MO_K_EXPERT + mode, s, [&] {
-        return pair ? launch_mode<true>(mode, f32, p, most_tiles, s) : launch_mode<false>(mode, f32, p, most_tiles, s);
+        const cudaError_t e = plan.pair ? launch_mode<true>(mode, f32, p, tiles, s) : launch_mode<false>(mode, f32, p, tiles, s);
+        if (e != cudaSuccess || !split) return e;
+        JoinArgs j;
+        j.part = parts;
+        j.out = q.out;
+        j.offsets = mode == kWgrad ? nullptr : q.offsets;
+        j.rows = rows_part;
+        j.cols = cols;
+        j.ld = ld_part;
+        j.ldo = q.ldo;
+        j.stride_o = q.stride_o;
+        j.matrix_rows = mode == kWgrad ? q.n : q.rows;
+        j.splits = plan.splits;
+        j.out_f32 = q.out_dtype == MO_F32;
+        j.accumulate = q.accumulate;
+        j.experts = q.experts;
+        const int64_t blocks = op_ceil_div(rows_part * (ld_part / 4), 256);
+        join_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 8 * kSms)), 256, 0, s>>>(j);
+        return cudaGetLastError();
     }));
 }
 
@@ -947,7 +1108,7 @@ int mo_debug_set_expert_pair(int on) {
 int expert_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k, int experts, size_t* bytes_out) {
     if (bytes_out == nullptr) return MO_ERR_INVALID_ARG;
     const int st = check_sizes(rows, n, k, experts);
-    if (st == MO_OK) *bytes_out = expert_ws_bytes();
+    if (st == MO_OK) *bytes_out = expert_ws_bytes(rows, n, k, experts);
     return st;
 }
 

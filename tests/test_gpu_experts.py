@@ -210,6 +210,39 @@ def test_gradients_match_differences():
         assert float(((Y[0].double() - Y[1].double()) * dY.double()).sum()) / 2 == float(want)   # integers below 2^24
 
 
+@pytest.mark.parametrize("out_dtype", [F32, BF16])
+@pytest.mark.parametrize("sizes,before,after,n,k", [
+    ([4100], 0, 0, 264, 200), ([3], 2, 1, 136, 8200), ([3], 0, 2, 8200, 72), ([5000, 0], 1, 4, 129, 77),
+    ([2051, 1], 0, 0, 257, 2056)])
+def test_long_sums_with_few_tiles_are_split_and_joined(sizes, before, after, n, k, out_dtype, geometry):
+    rng = np.random.default_rng(n * 3 + k)
+    E, off = len(sizes), _offsets(sizes, before)
+    R = int(off[-1]) + after
+    X, dY, W = _mat(rng, R, k), _mat(rng, R, n), _stack(rng, E, n, k)
+    o, ws = torch.from_numpy(off).to(dev()), _ws(R, n, k, E)
+    if max(n, k, max(sizes)) > 4000:
+        assert ws.numel() > 4096                       # room for the parts: some call is split
+    Y = torch.full((R, _pad8(n) + 8), 3.0, dtype=out_dtype, device=dev())
+    dX = torch.full((R, _pad8(k) + 8), 3.0, dtype=out_dtype, device=dev())
+    dW = _stack(rng, E, n, k, dtype=out_dtype, extra=8)
+    start = _f64(dW)
+    x, dy, w = _f64(X), _f64(dY), _f64(W)
+    for _ in range(2):                                 # a second call finds the first one's parts in the workspace
+        mo.expert_linear(X, W, o, Y[:, :n], ws)
+        mo.expert_linear_dgrad(dY, W, o, dX[:, :k], ws)
+    mo.expert_linear_wgrad(dY, X, o, dW, ws, accumulate=True)
+    _assert_close(Y[:, :n], ot.expert_linear(x, w, off), ot.expert_linear(np.abs(x), np.abs(w), off), k)
+    _assert_close(dX[:, :k], ot.expert_linear_dgrad(dy, w, off),
+                  ot.expert_linear_dgrad(np.abs(dy), np.abs(w), off), n)
+    _assert_close(dW, ot.expert_linear_wgrad(dy, x, off, start),
+                  ot.expert_linear_wgrad(np.abs(dy), np.abs(x), off, np.abs(start)), max(sizes))
+    assert torch.all(Y[:, n:] == 3.0) and torch.all(dX[:, k:] == 3.0)
+    out = np.ones(R, bool)
+    out[off[0]:off[-1]] = False
+    assert np.all(_f64(Y[:, :n])[out] == 0) and np.all(_f64(dX[:, :k])[out] == 0)
+    assert mo.mo_check_device_status(ws) == 0
+
+
 @pytest.mark.slow
 def test_large_sizes_against_float64_on_the_device():
     """Long groups, many tiles: sampled rows and columns."""
