@@ -247,6 +247,7 @@ template <int kRounds>
 __global__ void __launch_bounds__(kClusterThreads, 1)
 cluster_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, int digit_bits, uint32_t* keys_out,
                     uint32_t* pos_out) {
+    launch_dependents();
     extern __shared__ __align__(16) uint8_t smem_raw[];
     ClusterSmem& sm = *reinterpret_cast<ClusterSmem*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
@@ -447,6 +448,8 @@ __device__ __forceinline__ int64_t warp_lower_bound_key(const uint32_t* keys, in
 template <typename T, typename D, bool kWide>
 __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_constant__ GradArgs a) {
     constexpr int V = Elem<T>::kVec;
+    launch_dependents();
+    wait_for_previous();
     if (blockIdx.x >= a.sum_blocks) {                // rows of absent tokens: zeros
         const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - a.sum_blocks) * a.zero_rows;
         __shared__ uint8_t present[kMaxZeroRows];
@@ -541,6 +544,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_con
 constexpr int kJoinThreads = 256;
 template <typename T, typename D>
 __global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const __grid_constant__ GradArgs a) {
+    wait_for_previous();
     const int64_t chunk = blockIdx.x, first = chunk * a.chunk, next = first + a.chunk;
     if (next >= a.n) return;
     const uint32_t key = a.keys[next - 1], after = a.keys[next], head = a.keys[first];
@@ -610,18 +614,14 @@ cudaError_t launch_grad(const GradArgs& a0, cudaStream_t s) {
     const int64_t zero_blocks = a.accumulate ? 0 : op_ceil_div(a.vocab, a.zero_rows);
     if (a.sum_blocks + zero_blocks > 0) {
         const unsigned grid = static_cast<unsigned>(a.sum_blocks + zero_blocks);
-        if (wide_in)
-            grad_sum_kernel<T, D, true><<<grid, kGradThreads, 0, s>>>(a);
-        else
-            grad_sum_kernel<T, D, false><<<grid, kGradThreads, 0, s>>>(a);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = wide_in ? launch_after(grad_sum_kernel<T, D, true>, grid, kGradThreads, s, a)
+                                      : launch_after(grad_sum_kernel<T, D, false>, grid, kGradThreads, s, a);
         if (e != cudaSuccess) return e;
     }
     if (a.chunks > 1) {
         const int64_t by = op_ceil_div(a.dim, 2 * kJoinThreads);
-        grad_join_kernel<T, D><<<dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(by < 64 ? by : 64)),
-                                 kJoinThreads, 0, s>>>(a);
-        return cudaGetLastError();
+        return launch_after(grad_join_kernel<T, D>,
+                            dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(by < 64 ? by : 64)), kJoinThreads, s, a);
     }
     return cudaSuccess;
 }

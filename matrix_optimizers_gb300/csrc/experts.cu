@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Ctl* ctl = reinterpret_cast<Ctl*>(smem + kRingBytes + kEpiWarps * kOutBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (p.splits > 1) launch_dependents();
     const int cols = kMode == kFwd ? p.n : p.k;        // features of the output
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;   // rank 0 leads the pair
     const bool leader = rank == 0;
@@ -767,6 +768,7 @@ struct JoinArgs {
     int32_t splits, out_f32, accumulate, experts;
 };
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinArgs p) {
+    wait_for_previous();
     const int64_t groups = p.ld / 4, total = p.rows * groups;
     int64_t r0 = 0, r1 = p.rows;
     if (p.offsets != nullptr) {
@@ -1088,8 +1090,7 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
         j.accumulate = q.accumulate;
         j.experts = q.experts;
         const int64_t blocks = op_ceil_div(rows_part * (ld_part / 4), 256);
-        join_kernel<<<static_cast<unsigned>(std::min<int64_t>(blocks, 8 * kSms)), 256, 0, s>>>(j);
-        return cudaGetLastError();
+        return launch_after(join_kernel, static_cast<unsigned>(std::min<int64_t>(blocks, 8 * kSms)), 256, s, j);
     }));
 }
 

@@ -40,7 +40,28 @@ cudaError_t op_traced(int kind, cudaStream_t s, F&& launch) {
     return trace_end(kind, s) ? cudaSuccess : cudaErrorUnknown;
 }
 
+// Kernels of one call that follow each other: the later one's launch overlaps
+// the earlier one's end (programmatic dependent launch).  The earlier kernel calls
+// launch_dependents() when it starts, the later one wait_for_previous() before its
+// first access to anything that the earlier one writes or reads.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t s, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------- device side
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 template <typename T>
 struct Elem;
 template <>
