@@ -105,9 +105,10 @@ int mo_debug_inject_dep_stall(int matrix, int64_t wait_cycles);
 int mo_debug_cta_stamps(uint64_t* buf, int capacity, int max_ctas, int* recorded);
 
 /* Chooses the tile geometry of the expert products: 0 = 128 features x up to
- * 256 columns per CTA, 1 = 256 features per CTA pair (cta_group::2), -1 (the
- * default) = by the call's sizes.  Returns the previous setting + 1. */
-int mo_debug_set_expert_pair(int on);
+ * 256 columns per CTA, 1 = 256 features per CTA pair (cta_group::2), 2 = 128
+ * features x up to 32 tokens with a deeper ring (a weight gradient: as 0), -1
+ * (the default) = by the call's sizes.  Returns the previous setting + 1. */
+int mo_debug_set_expert_shape(int shape);
 
 /* Launch tracing, for measurement.  mo_trace_enable(capacity) makes every
  * later kernel launch of the calling thread (any entry point) record a CUDA

@@ -127,7 +127,7 @@ _SIGNATURES = [
     ("mo_debug_set_ns_fused", c_int32, [c_int32]),
     ("mo_debug_inject_dep_stall", c_int32, [c_int32, c_int64]),
     ("mo_debug_set_ns_pair", c_int32, [c_int32]),
-    ("mo_debug_set_expert_pair", c_int32, [c_int32]),
+    ("mo_debug_set_expert_shape", c_int32, [c_int32]),
     ("mo_debug_cta_stamps", c_int32, [c_void_p, c_int32, c_int32, ctypes.POINTER(c_int32)]),
     ("mo_trace_enable", c_int32, [c_int32]),
     ("mo_trace_read", c_int32, [ctypes.POINTER(c_int32), ctypes.POINTER(c_float), c_int32,
@@ -645,10 +645,10 @@ def mo_debug_set_ns_fused(on):
     return prev
 
 
-def mo_debug_set_expert_pair(on):
-    """Tile geometry of the expert products: 0 single CTAs, 1 CTA pairs, -1
-    (default) by the sizes; returns the previous setting."""
-    prev = load().mo_debug_set_expert_pair(int(on))
+def mo_debug_set_expert_shape(shape):
+    """Tile geometry of the expert products: 0 single CTAs, 1 CTA pairs, 2 few
+    tokens, -1 (default) by the sizes; returns the previous setting."""
+    prev = load().mo_debug_set_expert_shape(int(shape))
     _check(prev if prev < 0 else 0)
     return prev - 1
 

@@ -39,26 +39,39 @@ enum ExpertMode { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 constexpr int kBM = 128, kBN = 256, kBK = 64;             // lanes, columns and depth of one CTA's tile and stage
 constexpr int kABytes = kBM * kBK * 2;                    // 16 KB
 constexpr int kRingBytes = 196608;
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 9;
 // Single CTA (cta_group::1): a stage holds 128 features and up to 256 columns
 // (48 KB, four stages).  CTA pair (cta_group::2): 256 features x up to 256
 // columns per pair, each CTA holding its 128 features and half the columns
 // (32 KB, six stages), its own 128 x 256 accumulator and its own epilogue.
-template <bool kPair>
+// Few rows per expert: the weights are all there is to read, so tiles of up to 32
+// tokens and nine stages of 20 KB keep 144 KB of them in flight per SM instead of 64.
+// A weight gradient on single CTAs, which sums few rows and is bound by its stores,
+// gives a stage up for wider store blocks, two per epilogue warp.
+enum Shape { kSingle = 0, kPairs = 1, kFew = 2 };
+constexpr int shape_columns(int shape) { return shape == kFew ? 32 : kBN; }   // of a tile, at most
+constexpr int shape_features(int shape) { return shape == kPairs ? 2 * kBM : kBM; }
+template <int kMode, int kShape>
 struct Geo {
+    static constexpr bool kPair = kShape == kPairs, kWideOut = kMode == kWgrad && !kPair;
     static constexpr int kCtas = kPair ? 2 : 1;
-    static constexpr int kStageBytes = kABytes + kBN / kCtas * kBK * 2;
-    static constexpr int kStages = kRingBytes / kStageBytes;
-    static constexpr int kFeatures = kCtas * kBM;
-    static constexpr int kRound = kPair ? 32 : 16;        // columns of an MMA come in multiples of
+    static constexpr int kColumns = shape_columns(kShape), kFeatures = shape_features(kShape);
+    static constexpr int kStageBytes = kABytes + kColumns / kCtas * kBK * 2;
+    static constexpr int kStages = kRingBytes / kStageBytes - (kWideOut ? 1 : 0);
+    static constexpr int kOutRow = kWideOut ? 128 : 64;                       // wgrad: bytes of a store block's 32 rows
+    static constexpr int kOutBlocks = kWideOut ? 2 : 1;
+    static constexpr int kRound = kPair ? 32 : 16;                            // columns of an MMA come in multiples of
+    static_assert(kStages <= kMaxStages, "ring depth");
 };
-static_assert(Geo<true>::kStages <= kMaxStages && Geo<false>::kStages <= kMaxStages, "ring depth");
 constexpr int kEpiWarps = 8;
 constexpr int kProducerWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
-constexpr int kThreads = 32 * (kEpiWarps + 2);
+constexpr int kThreads = 32 * (kEpiWarps + 4);            // three warpgroups; two warps of the last have no role
+// Registers: the launch gives 168 to every thread; the last warpgroup keeps 56 of
+// them and the two epilogue warpgroups, which hold a tile's sums, take 224.
+constexpr int kLaunchRegs = 168, kIssueRegs = 56, kEpiRegs = 224;
+static_assert(4 * kIssueRegs + kEpiWarps * kEpiRegs <= (kThreads / 32) * kLaunchRegs, "register split");
 constexpr int kOutBytes = 2048;                           // one epilogue warp's store block
 constexpr int kMaxExperts = 1024;
-constexpr int kTokenGroup = 8;                            // token tiles that share a sweep over the features
 constexpr int kBoxes = 4;                                 // token boxes of 128, 64, 32 and 16 rows
 
 struct Ctl {
@@ -81,7 +94,7 @@ struct ExpertArgs {
     void* out;
     int64_t ldo, stride_o;
     int32_t rows, n, k, experts;
-    int32_t out_f32, accumulate;
+    int32_t group;                 // token tiles that share a sweep over the features, at most
     int32_t f_tiles;               // tiles over the output features
     int32_t width, c_tiles;        // wgrad: columns of a tile, tiles over the k columns
     int32_t splits;                // parts of every sum, each into an output of its own (joined afterwards)
@@ -113,12 +126,11 @@ __device__ __forceinline__ int tile_count(const ExpertArgs& p, const Ctl* ctl) {
 }
 
 // Tile u of the walk.  Forward and dgrad go expert by expert, within one in
-// groups of up to kTokenGroup token tiles, each sweeping the features with the
-// tokens innermost: the CTAs at work together then share a few thousand tokens
-// and features, which stay in L2.
-template <int kMode, bool kPair>
+// groups of token tiles, each sweeping the features with the tokens innermost: a
+// group's rows stay in L2 while every weight is read once for the group.
+template <int kMode, int kShape>
 __device__ __forceinline__ Tile tile_at(const ExpertArgs& p, const Ctl* ctl, int tile) {
-    using G = Geo<kPair>;
+    using G = Geo<kMode, kShape>;
     Tile t;
     uint32_t u = static_cast<uint32_t>(tile);
     t.split = 0;
@@ -143,12 +155,13 @@ __device__ __forceinline__ Tile tile_at(const ExpertArgs& p, const Ctl* ctl, int
         }
         t.e = lo;
         const int nt = ctl->cum[lo + 1] - ctl->cum[lo];
-        const uint32_t v = u - static_cast<uint32_t>(ctl->cum[lo]) * p.f_tiles, per = kTokenGroup * p.f_tiles;
+        const int group = ceil_div_i(nt, ceil_div_i(nt, p.group));             // equal groups
+        const uint32_t v = u - static_cast<uint32_t>(ctl->cum[lo]) * p.f_tiles, per = group * p.f_tiles;
         const int g = static_cast<int>(v / per);
-        const uint32_t w = v - g * per, gs = min(kTokenGroup, nt - g * kTokenGroup);
+        const uint32_t w = v - g * per, gs = min(group, nt - g * group);
         const int m = ctl->row[lo + 1] - ctl->row[lo], f = static_cast<int>(w / gs);
-        const int tok = g * kTokenGroup + static_cast<int>(w - f * gs);
-        const int size = (ceil_div_i(m, nt) + 15) / 16 * 16;                   // equal tiles, at most kBN tokens
+        const int tok = g * group + static_cast<int>(w - f * gs);
+        const int size = (ceil_div_i(m, nt) + G::kRound - 1) / G::kRound * G::kRound;   // equal tiles
         t.f0 = f * G::kFeatures;
         t.c0 = ctl->row[lo] + tok * size;
         t.cn = min(size, m - tok * size);
@@ -316,59 +329,60 @@ __device__ __forceinline__ void put_tokens(const ExpertArgs& p, int cols, int f,
     }
 }
 
-// Weight gradient: 32 rows (lanes) x 32 columns, staged with the 64-byte
-// swizzle of the store view (16-byte chunk c of row r at c ^ ((r >> 1) & 3)).
-template <bool kF32>
-__device__ __forceinline__ void put_weights(const ExpertArgs& p, int e, int row0, int col, float* v, uint32_t buf,
-                                            int lane) {
-    if (p.accumulate && row0 + lane < p.n) {
-        const int64_t at = e * p.stride_o + static_cast<int64_t>(row0 + lane) * p.ldo + col;
-        const int nv = min(32, p.k - col);
+// Weight gradient: column group g of a warp's four 32-column groups (pairs of
+// groups are neighbours, so that a 128-byte block of bf16 holds two).
+__device__ __forceinline__ int wgrad_column(int half, int g) { return (g >> 1) * 128 + half * 64 + (g & 1) * 32; }
+
+// The warp holds 32 rows (lanes) x its four groups.  They leave in blocks of 32
+// rows x kRow bytes, staged with the swizzle of the store view (16-byte chunk c of
+// row r at c ^ (r & 7) for 128-byte rows, c ^ ((r >> 1) & 3) for 64-byte rows).
+template <bool kF32, bool kAcc, int kRow, int kBlocks>
+__device__ __forceinline__ void put_weights(const ExpertArgs& p, int e, int row0, int c0, int cn, int half, float (&v)[4][32],
+                                            uint32_t buf0, int& block, int lane) {
+    constexpr int kCols = kRow / (kF32 ? 4 : 2), kPer = kF32 ? 4 : 8;   // columns of a block, of 16 bytes
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (j < nv)
-                v[j] += kF32 ? static_cast<const float*>(p.out)[at + j]
-                             : __bfloat162float(static_cast<const bf16*>(p.out)[at + j]);
-    }
-    if (col + 32 > p.k && p.k % (kF32 ? 4 : 8) != 0) {  // ends inside a 16-byte piece (see put_tokens)
-        if (row0 + lane >= p.n) return;
-        const int64_t at = e * p.stride_o + static_cast<int64_t>(row0 + lane) * p.ldo + col;
+    for (int b = 0; b < 128 / kCols; ++b) {
+        const int g0 = b * kCols / 32, j0 = b * kCols % 32, col = wgrad_column(half, g0) + j0;   // within the tile
+        if (col >= cn) continue;                       // warp-uniform
+        if (kAcc && row0 + lane < p.n) {
+            const int64_t at = e * p.stride_o + static_cast<int64_t>(row0 + lane) * p.ldo + c0 + col;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            if (col + j >= p.k) continue;
-            if (kF32)
-                static_cast<float*>(p.out)[at + j] = v[j];
-            else
-                static_cast<bf16*>(p.out)[at + j] = __float2bfloat16_rn(v[j]);
+            for (int j = 0; j < kCols; ++j)
+                if (col + j < cn)
+                    v[g0 + (j0 + j) / 32][(j0 + j) % 32] += kF32 ? static_cast<const float*>(p.out)[at + j]
+                                                                 : __bfloat162float(static_cast<const bf16*>(p.out)[at + j]);
         }
-        return;
-    }
-    constexpr int kCols = kF32 ? 16 : 32;              // columns of one 2 KB block
+        if (c0 + col + kCols > p.k && p.k % kPer != 0) {   // ends inside a 16-byte piece (see put_tokens)
+            if (row0 + lane < p.n) {
+                const int64_t at = e * p.stride_o + static_cast<int64_t>(row0 + lane) * p.ldo + c0 + col;
 #pragma unroll
-    for (int h = 0; h < 32 / kCols; ++h) {
-        if (col + h * kCols >= p.k) return;
-        if (elect_one()) bulk_wait_read_all();
+                for (int j = 0; j < kCols; ++j) {
+                    if (c0 + col + j >= p.k) continue;
+                    const float x = v[g0 + (j0 + j) / 32][(j0 + j) % 32];
+                    if (kF32)
+                        static_cast<float*>(p.out)[at + j] = x;
+                    else
+                        static_cast<bf16*>(p.out)[at + j] = __float2bfloat16_rn(x);
+                }
+            }
+            continue;
+        }
+        const uint32_t buf = buf0 + block * (32 * kRow);
+        block = block + 1 == kBlocks ? 0 : block + 1;
+        if (elect_one())                               // the store that last used the block has read it
+            asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kBlocks - 1) : "memory");
         __syncwarp();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint4 u;
-            if (kF32) {
-                float w[4];
+        for (int c = 0; c < kRow / 16; ++c) {
+            float w[kPer];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = v[(h * kCols + c * 4 + i) & 31];
-                u = pack16(w);
-            } else {
-                float w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = v[(c * 8 + i) & 31];
-                u = pack16(w);
-            }
-            sts_v4(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4), u);
+            for (int i = 0; i < kPer; ++i) w[i] = v[g0 + (j0 + c * kPer + i) / 32][(j0 + c * kPer + i) % 32];
+            sts_v4(buf + lane * kRow + ((kRow == 128 ? c ^ (lane & 7) : c ^ ((lane >> 1) & 3)) << 4), pack16(w));
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (elect_one()) {
-            tma_store_3d(&p.o, buf, col + h * kCols, row0, e);
+            tma_store_3d(&p.o, buf, c0 + col, row0, e);
             bulk_commit();
         }
     }
@@ -383,19 +397,21 @@ __device__ __forceinline__ void commit(uint32_t bar) {
         umma_commit(bar);
 }
 
-template <int kMode, bool kF32, bool kPair>
+template <int kMode, bool kF32, int kShape, bool kAcc>
 __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_constant__ ExpertArgs p) {
-    using G = Geo<kPair>;
+    using G = Geo<kMode, kShape>;
+    constexpr bool kPair = G::kPair;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Ctl* ctl = reinterpret_cast<Ctl*>(smem + kRingBytes + kEpiWarps * kOutBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (p.splits > 1) launch_dependents();
+    launch_dependents();                               // the next call of these operators may set up while this one ends
     const int cols = kMode == kFwd ? p.n : p.k;        // features of the output
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;   // rank 0 leads the pair
     const bool leader = rank == 0;
     const int unit = static_cast<int>(blockIdx.x) / G::kCtas, units = static_cast<int>(gridDim.x) / G::kCtas;
 
+    if (threadIdx.x < 3) tma_prefetch_desc(threadIdx.x == 0 ? &p.a : threadIdx.x == 1 ? &p.b[kBoxes - 1] : &p.o);
     if (threadIdx.x == kProducerWarp * 32) {
         for (int s = 0; s < G::kStages; ++s) {
             mbar_init(smem_u32(&ctl->full[s]), 1);
@@ -422,6 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             tmem_relinquish();
         }
     }
+    wait_for_previous();                               // everything above touches this CTA's own state only
     if (warp == 0) {                                   // the experts' rows and token tiles
         int carry = 0, top = 0;
         if (lane == 0) ctl->cum[0] = 0;
@@ -437,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             // the expert before ends where this one begins
             int before = __shfl_up_sync(0xffffffffu, a, 1);
             if (lane == 0) before = top;
-            int tiles = e > 0 && e <= p.experts ? (a - before + kBN - 1) / kBN : 0;
+            int tiles = e > 0 && e <= p.experts ? ceil_div_i(a - before, G::kColumns) : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(0xffffffffu, tiles, o);
@@ -459,205 +476,210 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
     volatile int* abort_flag = &ctl->abort_flag;
     const int tiles = tile_count<kMode>(p, ctl);
 
-    if (warp == kProducerWarp) {
-        int stage = 0;
-        uint32_t phase = 0, narmed = 0;
-        uint32_t tail_used = 0, tail_phase = 0;         // by stage: ragged last blocks armed, the parity of the last
-        bool ok = true;
-        for (int u = unit; u < tiles && ok; u += units) {
-            const Tile t = tile_at<kMode, kPair>(p, ctl, u);
-            // this CTA's features and columns
-            const int f0 = t.f0 + static_cast<int>(rank) * kBM;
-            const int mine = t.nmma / G::kCtas, c0 = t.c0 + static_cast<int>(rank) * mine;
-            const int nb = (mine + 63) / 64;                         // wgrad: 64-wide boxes of X
-            const uint32_t bytes = kABytes + (kMode == kWgrad ? nb * 8192 : mine * kBK * 2);
-            for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                if (!warp_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err, 0x201)) {
-                    ok = false;
-                    break;
-                }
-                // The pair's copies count on the leader's barrier, except that a weight
-                // gradient's ragged last block counts on each CTA's own, because each
-                // zeroes its part before the leader may use it; the stage's full barrier
-                // then only turns its phase over.
-                const bool tail = kPair && kMode == kWgrad && (kb + 1) * kBK > t.depth;
-                if (tail) {
-                    tail_phase ^= (tail_used >> stage & 1u) << stage;
-                    tail_used |= 1u << stage;
-                }
-                if (elect_one()) {
-                    const uint32_t full = smem_u32(&ctl->full[stage]);
-                    uint32_t bar = kPair ? mapa_shared(full, 0) : full;
-                    if (tail) {
-                        if (leader) mbar_arrive(full);
-                        bar = smem_u32(&ctl->tail[stage]);
-                        mbar_arrive_expect_tx(bar, bytes);
-                        bar = mapa_shared(bar, rank);
-                    } else if (leader) {
-                        mbar_arrive_expect_tx(full, G::kCtas * bytes);
-                    }
-                    const uint32_t sa = smem_u32(smem + stage * G::kStageBytes);
-                    const uint32_t sb = sa + kABytes;
-                    const int k0 = kb * kBK;
-                    if (kMode == kFwd) {
-                        load3<kPair>(sa, &p.a, bar, k0, f0, t.e);
-                    } else if (kMode == kDgrad) {
-                        load3<kPair>(sa, &p.a, bar, f0, k0, t.e);
-                        load3<kPair>(sa + 8192, &p.a, bar, f0 + 64, k0, t.e);
-                    } else {
-                        load2<kPair>(sa, &p.a, bar, f0, t.r0 + k0);
-                        load2<kPair>(sa + 8192, &p.a, bar, f0 + 64, t.r0 + k0);
-                        for (int i = 0; i < nb; ++i)
-                            load2<kPair>(sb + i * 8192, &p.b[0], bar, c0 + i * 64, t.r0 + k0);
-                    }
-                    if (kMode != kWgrad) {
-                        // the tokens as boxes of 128, 64, 32 and 16 rows
-                        int at = 0;
-                        if (!kPair && mine == 256) {
-                            load2<kPair>(sb, &p.b[0], bar, k0, c0);
-                            at = 128;
-                        }
-#pragma unroll
-                        for (int i = 0; i < kBoxes; ++i) {
-                            const int r = 128 >> i;
-                            if (mine - at >= r) {
-                                load2<kPair>(sb + at * 128, &p.b[i], bar, k0, c0 + at);
-                                at += r;
-                            }
-                        }
-                    }
-                }
-                __syncwarp();
-                ++narmed;
-                if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-            }
-        }
-        if (lane == 0) {
-            // every armed copy lands before the CTA exits, also when the MMA warp gave up
-            // first; the leader's barriers also count the peer's copies
-            if (leader) {
-                for (int s = 0; s < G::kStages; ++s) {
-                    if (narmed <= static_cast<uint32_t>(s)) continue;
-                    const uint32_t times = (narmed - 1u - static_cast<uint32_t>(s)) / G::kStages + 1u;
-                    const long long t0 = clock64();
-                    while (!mbar_try_wait(smem_u32(&ctl->full[s]), (times - 1u) & 1u) && clock64() - t0 < kWaitCycles) {}
-                }
-            } else if (!ok) {
-                // copies that count on the leader's barriers: time to land (~2 ms, far above
-                // a copy's latency); the closing cluster barrier keeps this CTA until the leader is done
-                const long long t0 = clock64();
-                while (clock64() - t0 < (1LL << 22)) {}
-            }
-            for (int s = 0; s < G::kStages; ++s) {
-                if (!(tail_used >> s & 1u)) continue;
-                const long long t0 = clock64();
-                while (!mbar_try_wait(smem_u32(&ctl->tail[s]), tail_phase >> s & 1u) && clock64() - t0 < kWaitCycles) {}
-            }
-        }
-    } else if (warp == kMmaWarp && leader) {
-        int stage = 0;
-        uint32_t phase = 0, tail_phase = 0;             // tail_phase: by stage
-        bool ok = true;
-        int q = 0;                                      // chunks so far: accumulator ping-pong
-        for (int u = unit; u < tiles && ok; u += units) {
-            const Tile t = tile_at<kMode, kPair>(p, ctl, u);
-            const uint32_t idesc = instr_desc(G::kFeatures, t.nmma, kMode != kFwd, kMode == kWgrad);
-            // K-major operands: 8-row groups 1 KB apart, 32 bytes per 16-wide step.
-            // MN-major operands: 64-column blocks 8 KB apart, 8-row K groups 1 KB
-            // apart, two of them (2 KB) per step.
-            const uint64_t ad0 = kMode == kFwd ? sdesc_sw128(0, 16, 1024) : sdesc_sw128(0, 8192, 1024);
-            const uint64_t bd0 = kMode == kWgrad ? sdesc_sw128(0, 8192, 1024) : sdesc_sw128(0, 16, 1024);
-            constexpr uint32_t a_step = (kMode == kFwd ? 32 : 2048) >> 4, b_step = (kMode == kWgrad ? 2048 : 32) >> 4;
-            int in_chunk = 0;
-            for (int kb = t.kb0; kb < t.kb1; ++kb) {
-                if (in_chunk == 0 &&
-                    !warp_wait(smem_u32(&ctl->tempty[q & 1]), ((q >> 1) & 1) ^ 1u, abort_flag, p.err, 0x202)) {
-                    ok = false;
-                    break;
-                }
-                if (!warp_wait(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err, 0x203)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t sa = smem_u32(smem + stage * G::kStageBytes), sb = sa + kABytes;
-                int steps = kBK / 16;
-                if (kMode == kWgrad && (kb + 1) * kBK > t.depth) {              // the sum ends inside this block
-                    const int v = t.depth - kb * kBK, boxes = 2 + (t.nmma / G::kCtas + 63) / 64;
-                    steps = (v + 15) / 16;
-                    if (kPair && !warp_wait(smem_u32(&ctl->tail[stage]), tail_phase >> stage & 1u, abort_flag, p.err, 0x205)) {
+    if (warp >= kEpiWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+        if (warp == kProducerWarp) {
+            int stage = 0;
+            uint32_t phase = 0, narmed = 0;
+            uint32_t tail_used = 0, tail_phase = 0;         // by stage: ragged last blocks armed, the parity of the last
+            bool ok = true;
+            for (int u = unit; u < tiles && ok; u += units) {
+                const Tile t = tile_at<kMode, kShape>(p, ctl, u);
+                // this CTA's features and columns
+                const int f0 = t.f0 + static_cast<int>(rank) * kBM;
+                const int mine = t.nmma / G::kCtas, c0 = t.c0 + static_cast<int>(rank) * mine;
+                const int nb = (mine + 63) / 64;                         // wgrad: 64-wide boxes of X
+                const uint32_t bytes = kABytes + (kMode == kWgrad ? nb * 8192 : mine * kBK * 2);
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (!warp_wait(smem_u32(&ctl->empty[stage]), phase ^ 1u, abort_flag, p.err, 0x201)) {
                         ok = false;
                         break;
                     }
-                    zero_tail(sa, boxes, v, lane);
-                    if (kPair) {
-                        bool there = mbar_wait_cluster_bounded(smem_u32(&ctl->tail_peer[stage]), tail_phase >> stage & 1u,
-                                                               abort_flag, p.err, 0x206);
-                        if (!__all_sync(0xffffffffu, there)) {
+                    // The pair's copies count on the leader's barrier, except that a weight
+                    // gradient's ragged last block counts on each CTA's own, because each
+                    // zeroes its part before the leader may use it; the stage's full barrier
+                    // then only turns its phase over.
+                    const bool tail = kPair && kMode == kWgrad && (kb + 1) * kBK > t.depth;
+                    if (tail) {
+                        tail_phase ^= (tail_used >> stage & 1u) << stage;
+                        tail_used |= 1u << stage;
+                    }
+                    if (elect_one()) {
+                        const uint32_t full = smem_u32(&ctl->full[stage]);
+                        uint32_t bar = kPair ? mapa_shared(full, 0) : full;
+                        if (tail) {
+                            if (leader) mbar_arrive(full);
+                            bar = smem_u32(&ctl->tail[stage]);
+                            mbar_arrive_expect_tx(bar, bytes);
+                            bar = mapa_shared(bar, rank);
+                        } else if (leader) {
+                            mbar_arrive_expect_tx(full, G::kCtas * bytes);
+                        }
+                        const uint32_t sa = smem_u32(smem + stage * G::kStageBytes);
+                        const uint32_t sb = sa + kABytes;
+                        const int k0 = kb * kBK;
+                        if (kMode == kFwd) {
+                            load3<kPair>(sa, &p.a, bar, k0, f0, t.e);
+                        } else if (kMode == kDgrad) {
+                            load3<kPair>(sa, &p.a, bar, f0, k0, t.e);
+                            load3<kPair>(sa + 8192, &p.a, bar, f0 + 64, k0, t.e);
+                        } else {
+                            load2<kPair>(sa, &p.a, bar, f0, t.r0 + k0);
+                            load2<kPair>(sa + 8192, &p.a, bar, f0 + 64, t.r0 + k0);
+                            for (int i = 0; i < nb; ++i)
+                                load2<kPair>(sb + i * 8192, &p.b[0], bar, c0 + i * 64, t.r0 + k0);
+                        }
+                        if (kMode != kWgrad) {
+                            // the tokens as boxes of 128, 64, 32 and 16 rows
+                            int at = 0;
+                            if (kShape == kSingle && mine == 256) {
+                                load2<kPair>(sb, &p.b[0], bar, k0, c0);
+                                at = 128;
+                            }
+#pragma unroll
+                            for (int i = 0; i < kBoxes; ++i) {
+                                const int r = 128 >> i;
+                                if (mine - at >= r) {
+                                    load2<kPair>(sb + at * 128, &p.b[i], bar, k0, c0 + at);
+                                    at += r;
+                                }
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    ++narmed;
+                    if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (lane == 0) {
+                // every armed copy lands before the CTA exits, also when the MMA warp gave up
+                // first; the leader's barriers also count the peer's copies
+                if (leader) {
+                    for (int s = 0; s < G::kStages; ++s) {
+                        if (narmed <= static_cast<uint32_t>(s)) continue;
+                        const uint32_t times = (narmed - 1u - static_cast<uint32_t>(s)) / G::kStages + 1u;
+                        const long long t0 = clock64();
+                        while (!mbar_try_wait(smem_u32(&ctl->full[s]), (times - 1u) & 1u) && clock64() - t0 < kWaitCycles) {}
+                    }
+                } else if (!ok) {
+                    // copies that count on the leader's barriers: time to land (~2 ms, far above
+                    // a copy's latency); the closing cluster barrier keeps this CTA until the leader is done
+                    const long long t0 = clock64();
+                    while (clock64() - t0 < (1LL << 22)) {}
+                }
+                for (int s = 0; s < G::kStages; ++s) {
+                    if (!(tail_used >> s & 1u)) continue;
+                    const long long t0 = clock64();
+                    while (!mbar_try_wait(smem_u32(&ctl->tail[s]), tail_phase >> s & 1u) && clock64() - t0 < kWaitCycles) {}
+                }
+            }
+        } else if (warp == kMmaWarp && leader) {
+            int stage = 0;
+            uint32_t phase = 0, tail_phase = 0;             // tail_phase: by stage
+            bool ok = true;
+            int q = 0;                                      // chunks so far: accumulator ping-pong
+            for (int u = unit; u < tiles && ok; u += units) {
+                const Tile t = tile_at<kMode, kShape>(p, ctl, u);
+                const uint32_t idesc = instr_desc(G::kFeatures, t.nmma, kMode != kFwd, kMode == kWgrad);
+                // K-major operands: 8-row groups 1 KB apart, 32 bytes per 16-wide step.
+                // MN-major operands: 64-column blocks 8 KB apart, 8-row K groups 1 KB
+                // apart, two of them (2 KB) per step.
+                const uint64_t ad0 = kMode == kFwd ? sdesc_sw128(0, 16, 1024) : sdesc_sw128(0, 8192, 1024);
+                const uint64_t bd0 = kMode == kWgrad ? sdesc_sw128(0, 8192, 1024) : sdesc_sw128(0, 16, 1024);
+                constexpr uint32_t a_step = (kMode == kFwd ? 32 : 2048) >> 4, b_step = (kMode == kWgrad ? 2048 : 32) >> 4;
+                int in_chunk = 0;
+                for (int kb = t.kb0; kb < t.kb1; ++kb) {
+                    if (in_chunk == 0 &&
+                        !warp_wait(smem_u32(&ctl->tempty[q & 1]), ((q >> 1) & 1) ^ 1u, abort_flag, p.err, 0x202)) {
+                        ok = false;
+                        break;
+                    }
+                    if (!warp_wait(smem_u32(&ctl->full[stage]), phase, abort_flag, p.err, 0x203)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t sa = smem_u32(smem + stage * G::kStageBytes), sb = sa + kABytes;
+                    int steps = kBK / 16;
+                    if (kMode == kWgrad && (kb + 1) * kBK > t.depth) {              // the sum ends inside this block
+                        const int v = t.depth - kb * kBK, boxes = 2 + (t.nmma / G::kCtas + 63) / 64;
+                        steps = (v + 15) / 16;
+                        if (kPair && !warp_wait(smem_u32(&ctl->tail[stage]), tail_phase >> stage & 1u, abort_flag, p.err, 0x205)) {
                             ok = false;
                             break;
                         }
-                        tail_phase ^= 1u << stage;
+                        zero_tail(sa, boxes, v, lane);
+                        if (kPair) {
+                            bool there = mbar_wait_cluster_bounded(smem_u32(&ctl->tail_peer[stage]), tail_phase >> stage & 1u,
+                                                                   abort_flag, p.err, 0x206);
+                            if (!__all_sync(0xffffffffu, there)) {
+                                ok = false;
+                                break;
+                            }
+                            tail_phase ^= 1u << stage;
+                        }
                     }
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t d = tmem + static_cast<uint32_t>((q & 1) * kBN);
-                    auto mma = [&](int k) {
-                        const uint64_t ad = ad0 + ((sa >> 4) + k * a_step), bd = bd0 + ((sb >> 4) + k * b_step);
-                        if constexpr (kPair)
-                            umma_bf16_pair(d, ad, bd, idesc, (in_chunk | k) != 0 ? 1u : 0u);
-                        else
-                            umma_bf16(d, ad, bd, idesc, (in_chunk | k) != 0 ? 1u : 0u);
-                    };
-                    if (steps == kBK / 16) {
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint32_t d = tmem + static_cast<uint32_t>((q & 1) * kBN);
+                        auto mma = [&](int k) {
+                            const uint64_t ad = ad0 + ((sa >> 4) + k * a_step), bd = bd0 + ((sb >> 4) + k * b_step);
+                            if constexpr (kPair)
+                                umma_bf16_pair(d, ad, bd, idesc, (in_chunk | k) != 0 ? 1u : 0u);
+                            else
+                                umma_bf16(d, ad, bd, idesc, (in_chunk | k) != 0 ? 1u : 0u);
+                        };
+                        if (steps == kBK / 16) {
 #pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k) mma(k);
-                    } else {
-                        for (int k = 0; k < steps; ++k) mma(k);
+                            for (int k = 0; k < kBK / 16; ++k) mma(k);
+                        } else {
+                            for (int k = 0; k < steps; ++k) mma(k);
+                        }
+                        commit<kPair>(smem_u32(&ctl->empty[stage]));
+                        if (in_chunk + 1 == p.chunk || kb + 1 == t.kb1) commit<kPair>(smem_u32(&ctl->tfull[q & 1]));
                     }
-                    commit<kPair>(smem_u32(&ctl->empty[stage]));
-                    if (in_chunk + 1 == p.chunk || kb + 1 == t.kb1) commit<kPair>(smem_u32(&ctl->tfull[q & 1]));
-                }
-                __syncwarp();
-                if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-                if (++in_chunk == p.chunk || kb + 1 == t.kb1) {
-                    ++q;
-                    in_chunk = 0;
+                    __syncwarp();
+                    if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+                    if (++in_chunk == p.chunk || kb + 1 == t.kb1) {
+                        ++q;
+                        in_chunk = 0;
+                    }
                 }
             }
-        }
-        if (elect_one()) {                              // all issued MMAs complete before TMEM is released
-            commit<kPair>(smem_u32(&ctl->drain));
-            const long long t0 = clock64();
-            while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < kWaitCycles) {}
-        }
-    } else if (warp == kMmaWarp) {
-        // the pair's second CTA: zeroes its part of each ragged last block
-        if (kMode == kWgrad) {
-            uint32_t tail_phase = 0;                    // by stage
-            int64_t blocks = 0;                         // K blocks so far: the ring's position
-            for (int u = unit; u < tiles; u += units) {
-                const Tile t = tile_at<kMode, kPair>(p, ctl, u);
-                blocks += t.kb1 - t.kb0;
-                if (t.kb1 == t.kb0 || t.kb1 * kBK <= t.depth) continue;
-                const int stage = static_cast<int>((blocks - 1) % G::kStages);
-                bool there = true;
-                if (lane == 0)
-                    there = mbar_wait_bounded(smem_u32(&ctl->tail[stage]), tail_phase >> stage & 1u, abort_flag, p.err, 0x207);
-                if (!__shfl_sync(0xffffffffu, there, 0)) break;
-                tail_phase ^= 1u << stage;
-                __syncwarp();
-                zero_tail(smem_u32(smem + stage * G::kStageBytes), 2 + (t.nmma / 2 + 63) / 64, t.depth % kBK, lane);
-                if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tail_peer[stage]), 0));
+            if (elect_one()) {                              // all issued MMAs complete before TMEM is released
+                commit<kPair>(smem_u32(&ctl->drain));
+                const long long t0 = clock64();
+                while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < kWaitCycles) {}
             }
-        }
-        if (lane == 0) {                                // the leader's MMAs write this CTA's accumulators
-            const long long t0 = clock64();
-            while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < kWaitCycles) {}
+        } else if (warp == kMmaWarp) {
+            // the pair's second CTA: zeroes its part of each ragged last block
+            if (kMode == kWgrad) {
+                uint32_t tail_phase = 0;                    // by stage
+                int64_t blocks = 0;                         // K blocks so far: the ring's position
+                for (int u = unit; u < tiles; u += units) {
+                    const Tile t = tile_at<kMode, kShape>(p, ctl, u);
+                    blocks += t.kb1 - t.kb0;
+                    if (t.kb1 == t.kb0 || t.kb1 * kBK <= t.depth) continue;
+                    const int stage = static_cast<int>((blocks - 1) % G::kStages);
+                    bool there = true;
+                    if (lane == 0)
+                        there = mbar_wait_bounded(smem_u32(&ctl->tail[stage]), tail_phase >> stage & 1u, abort_flag, p.err, 0x207);
+                    if (!__shfl_sync(0xffffffffu, there, 0)) break;
+                    tail_phase ^= 1u << stage;
+                    __syncwarp();
+                    zero_tail(smem_u32(smem + stage * G::kStageBytes), 2 + (t.nmma / 2 + 63) / 64, t.depth % kBK, lane);
+                    if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&ctl->tail_peer[stage]), 0));
+                }
+            }
+            if (lane == 0) {                                // the leader's MMAs write this CTA's accumulators
+                const long long t0 = clock64();
+                while (!mbar_try_wait(smem_u32(&ctl->drain), 0) && clock64() - t0 < kWaitCycles) {}
+            }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         const int quarter = warp & 3, half = warp >> 2;
-        const uint32_t buf = smem_u32(smem + kRingBytes + warp * kOutBytes);
+        const uint32_t buf = smem_u32(smem + G::kStages * G::kStageBytes + warp * G::kOutBlocks * 32 * G::kOutRow);
+        int block = 0;                                  // wgrad: the store block in turn
         if (kMode != kWgrad && p.splits == 1) {         // rows of no expert
             const int head = ctl->row[0], tail = ctl->row[p.experts];
             const int64_t extra = static_cast<int64_t>(head) + (p.rows - tail);
@@ -678,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
         for (int u = unit; u < tiles && ok; u += units) {
             int chunks, nmma;
             {
-                const Tile t = tile_at<kMode, kPair>(p, ctl, u);
+                const Tile t = tile_at<kMode, kShape>(p, ctl, u);
                 chunks = ceil_div_i(t.kb1 - t.kb0, p.chunk);
                 nmma = t.nmma;
             }
@@ -693,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
                 tc_fence_after();
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int col = (2 * g + half) * 32;
+                    const int col = kMode == kWgrad ? wgrad_column(half, g) : (2 * g + half) * 32;
                     if (col >= nmma) continue;          // warp-uniform
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -714,19 +736,21 @@ __global__ void __launch_bounds__(kThreads, 1) expert_kernel(const __grid_consta
             if (!ok) break;
             int again = u;                              // the tile's place once more: holding it over the sums spills registers
             asm volatile("" : "+r"(again));
-            const Tile t = tile_at<kMode, kPair>(p, ctl, again);
-            if (kMode == kWgrad && t.depth == 0 && p.accumulate) continue;
+            const Tile t = tile_at<kMode, kShape>(p, ctl, again);
+            if (kAcc && t.depth == 0) continue;
             const int f = t.f0 + static_cast<int>(rank) * kBM + quarter * 32;
             if (f >= (kMode == kWgrad ? p.n : cols)) continue;
+            if constexpr (kMode == kWgrad) {
+                put_weights<kF32, kAcc, G::kOutRow, G::kOutBlocks>(p, t.split * p.experts + t.e, f, t.c0, t.cn, half, v, buf, block,
+                                                             lane);
+            } else {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int col = (2 * g + half) * 32;
-                if (col >= t.cn) continue;
-                if (kMode == kWgrad)
-                    put_weights<kF32>(p, t.split * p.experts + t.e, f, t.c0 + col, v[g], buf, lane);
-                else
+                for (int g = 0; g < 4; ++g) {
+                    const int col = (2 * g + half) * 32;
+                    if (col >= t.cn) continue;
                     put_tokens<kF32>(p, cols, f, static_cast<int64_t>(t.split) * p.rows + t.c0 + col, min(32, t.cn - col),
                                      v[g], buf, lane);
+                }
             }
         }
         if (elect_one()) bulk_wait_all();               // no store still reads this CTA's shared memory
@@ -854,17 +878,17 @@ struct Request {
 };
 
 // CTAs of one launch: one per SM, or as many pairs as the device holds at once.
-template <int kMode, bool kF32, bool kPair>
+template <int kMode, bool kF32, int kShape, bool kAcc>
 cudaError_t prepare_expert(int* ctas) {
     static std::atomic<int> known[64];                  // by device ordinal; 0: not asked yet
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if ((*ctas = known[dev & 63].load()) > 0) return cudaSuccess;
-    e = cudaFuncSetAttribute(expert_kernel<kMode, kF32, kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    e = cudaFuncSetAttribute(expert_kernel<kMode, kF32, kShape, kAcc>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     if (e != cudaSuccess) return e;
     *ctas = device_sm_count();
-    if (kPair) {
+    if (kShape == kPairs) {
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -876,7 +900,7 @@ cudaError_t prepare_expert(int* ctas) {
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
         int pairs = 0;
-        e = cudaOccupancyMaxActiveClusters(&pairs, expert_kernel<kMode, kF32, kPair>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&pairs, expert_kernel<kMode, kF32, kShape, kAcc>, &cfg);
         if (e != cudaSuccess) return e;
         if (pairs < 1) return cudaErrorInvalidConfiguration;
         *ctas = std::min(2 * pairs, *ctas / 2 * 2);
@@ -885,39 +909,44 @@ cudaError_t prepare_expert(int* ctas) {
     return cudaSuccess;
 }
 
-template <int kMode, bool kF32, bool kPair>
+template <int kMode, bool kF32, int kShape, bool kAcc = false>
 cudaError_t launch_expert(const ExpertArgs& p, int64_t most_tiles, cudaStream_t s) {
     int ctas = 0;
-    const cudaError_t e = prepare_expert<kMode, kF32, kPair>(&ctas);
+    const cudaError_t e = prepare_expert<kMode, kF32, kShape, kAcc>(&ctas);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr;
-    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most_tiles * Geo<kPair>::kCtas, ctas)));
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(most_tiles * (kShape == kPairs ? 2 : 1), ctas)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
-    if (kPair) {
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = 2;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (kShape == kPairs) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, expert_kernel<kMode, kF32, kPair>, p);
+    return cudaLaunchKernelEx(&cfg, expert_kernel<kMode, kF32, kShape, kAcc>, p);
 }
 
-template <bool kPair>
-cudaError_t launch_mode(int mode, bool f32, const ExpertArgs& p, int64_t most_tiles, cudaStream_t s) {
-    if (mode == kFwd)
-        return f32 ? launch_expert<kFwd, true, kPair>(p, most_tiles, s) : launch_expert<kFwd, false, kPair>(p, most_tiles, s);
-    if (mode == kDgrad)
-        return f32 ? launch_expert<kDgrad, true, kPair>(p, most_tiles, s)
-                   : launch_expert<kDgrad, false, kPair>(p, most_tiles, s);
-    return f32 ? launch_expert<kWgrad, true, kPair>(p, most_tiles, s) : launch_expert<kWgrad, false, kPair>(p, most_tiles, s);
+template <int kShape>
+cudaError_t launch_product(int mode, bool f32, const ExpertArgs& p, int64_t tiles, cudaStream_t s) {
+    if (mode == kFwd) return f32 ? launch_expert<kFwd, true, kShape>(p, tiles, s) : launch_expert<kFwd, false, kShape>(p, tiles, s);
+    return f32 ? launch_expert<kDgrad, true, kShape>(p, tiles, s) : launch_expert<kDgrad, false, kShape>(p, tiles, s);
+}
+template <int kShape>
+cudaError_t launch_wgrad(bool f32, bool acc, const ExpertArgs& p, int64_t tiles, cudaStream_t s) {
+    if (acc)
+        return f32 ? launch_expert<kWgrad, true, kShape, true>(p, tiles, s) : launch_expert<kWgrad, false, kShape, true>(p, tiles, s);
+    return f32 ? launch_expert<kWgrad, true, kShape>(p, tiles, s) : launch_expert<kWgrad, false, kShape>(p, tiles, s);
 }
 
-// -1: chosen by the call's sizes; 0 / 1: single CTAs / CTA pairs (tests, measurements).
-std::atomic<int> g_expert_pair{-1};
+// -1: chosen by the call's sizes; else a Shape (tests, measurements).
+std::atomic<int> g_expert_shape{-1};
 
 // A float32 result's sums leave TMEM every kF32Chunk K blocks (768 terms): the
 // tensor core's accumulator drops bits below its last place, always towards zero,
@@ -935,38 +964,47 @@ constexpr size_t kExpertHeader = 256;      // the error word that mo_check_devic
 
 // How a call runs: on CTA pairs or single CTAs, and in how many parts each sum.
 struct Plan {
-    bool pair;
+    int shape;
     int splits;
 };
 
 // Tiles of a call at most (each expert may end in a tile of its own).
-int64_t most_tiles(int mode, int64_t rows, int64_t n, int64_t k, int experts, bool pair) {
-    const int64_t features = pair ? 2 * kBM : kBM;
+int64_t most_tiles(int mode, int64_t rows, int64_t n, int64_t k, int experts, int shape) {
+    const int64_t features = shape_features(shape);
     if (mode == kWgrad) return experts * op_ceil_div(n, features) * op_ceil_div(k, kBN);
-    return (rows / kBN + std::min<int64_t>(experts, rows)) * op_ceil_div(mode == kFwd ? n : k, features);
+    return (rows / shape_columns(shape) + std::min<int64_t>(experts, rows)) * op_ceil_div(mode == kFwd ? n : k, features);
 }
 
 constexpr int64_t kSms = 152;
-constexpr int64_t kShortSum = 512;         // rows per expert from which a weight gradient runs on pairs
+constexpr int64_t kShortSum = 256;         // rows per expert from which a weight gradient runs on pairs
+constexpr int64_t kFewRows = 16;           // rows per expert up to which the weights set the time
+constexpr int64_t kFewTiles = 228;         // narrow tiles of a product so small that more CTAs help it most
 constexpr int64_t kSplitBlocks = 24;       // K blocks that a split has to take off a tile's time
 constexpr int64_t kMinSplitBlocks = 4;     // K blocks of a part, at least
 
 // Pairs halve the operand bytes per SM; a weight gradient over few rows is bound by
-// its stores instead, which single CTAs (more of them, each waiting for itself alone)
-// issue faster.  Measured (us, single / pair): forward of 16384 rows, 8 experts of
-// 4096 x 4096 334 / 296; 64 rows, 8 experts of 4096 x 4096 49 / 46; 16 rows, 16 experts of
-// 2048 x 1024 8.1 / 8.9; float32 weight gradient over 1024 rows each, 16 experts of 2048 x
-// 2048 138 / 126; over 512 (32 of 1024 x 1024) 50.7 / 51.9; over 256 (16 of 2048 x 2048) 69 / 75.
+// its stores instead, which single CTAs issue faster; narrow tiles give small products
+// more CTAs.  Measured (us, single / pair / narrow): forward of 16384 rows, 8 experts of
+// 4096 x 4096 332 / 294 / -; 4096 rows, 16 experts of 2048 x 2048 44 / 39 / 140; 512 rows, 8
+// experts of 1024 x 1024 9.9 / 10.1 / 9.1; 256 rows of one 768 x 768 9.3 / 9.7 / 7.2; 64
+// rows, 8 experts of 4096 x 4096 49 / 46 / 47; 16 rows, 16 experts of 2048 x 1024 9.1 / 9.7 /
+// 9.1 with the weights in L2.  Weight gradients, float32 and bf16, 16 experts of 2048 x
+// 2048 over 1024 rows each 148 / 116 and 130 / 104, over 256 70 / 68 and 55 / 51, over
+// 64 49 / 59 and 32 / 42.
 // Where the tiles leave at least half of the SMs idle and the sums are long, each sum is
 // split into parts that are joined in order afterwards (about 3 us more).
 Plan plan_call(int mode, int64_t rows, int64_t n, int64_t k, int experts, int forced) {
     const int64_t depth = mode == kFwd ? k : mode == kDgrad ? n : op_ceil_div(rows, experts);
     const int64_t blocks = op_ceil_div(depth, kBK);
     Plan p;
-    p.pair = mode == kWgrad ? depth >= kShortSum
-                            : depth > 1024 || most_tiles(mode, rows, n, k, experts, true) > 2 * (kSms / 2);
-    if (forced >= 0) p.pair = forced == 1;
-    const int64_t tiles = most_tiles(mode, rows, n, k, experts, p.pair), units = p.pair ? kSms / 2 : kSms;
+    if (mode == kWgrad)
+        p.shape = depth >= kShortSum ? kPairs : kSingle;
+    else if (rows <= kFewRows * experts || most_tiles(mode, rows, n, k, experts, kFew) <= kFewTiles)
+        p.shape = kFew;
+    else
+        p.shape = depth > 1024 || most_tiles(mode, rows, n, k, experts, kPairs) > 2 * (kSms / 2) ? kPairs : kSingle;
+    if (forced >= 0) p.shape = mode == kWgrad && forced == kFew ? kSingle : forced;
+    const int64_t tiles = most_tiles(mode, rows, n, k, experts, p.shape), units = p.shape == kPairs ? kSms / 2 : kSms;
     p.splits = 1;
     if (tiles > 0 && 2 * tiles <= units) {
         const int64_t s = std::min(units / tiles, blocks / kMinSplitBlocks);
@@ -982,7 +1020,7 @@ int64_t part_ld(int mode, int64_t n, int64_t k) { return op_ceil_div(mode == kFw
 size_t expert_ws_bytes(int64_t rows, int64_t n, int64_t k, int experts) {
     size_t most = 0;
     for (int mode = kFwd; mode <= kWgrad; ++mode)
-        for (int forced = 0; forced < 2; ++forced) {
+        for (int forced = kSingle; forced <= kFew; ++forced) {
             const Plan p = plan_call(mode, rows, n, k, experts, forced);
             if (p.splits > 1)
                 most = std::max(most, static_cast<size_t>(p.splits) * static_cast<size_t>(part_rows(mode, rows, n, experts)) *
@@ -1028,7 +1066,8 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
         }));
     }
     if (!get_encode()) return MO_ERR_CUDA;
-    const Plan plan = plan_call(mode, q.rows, q.n, q.k, q.experts, g_expert_pair.load());
+    const Plan plan = plan_call(mode, q.rows, q.n, q.k, q.experts, g_expert_shape.load());
+    const bool pair = plan.shape == kPairs;
     const bool split = plan.splits > 1;
     const bool f32 = split || q.out_dtype == MO_F32;    // of what the product kernel writes
     float* parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kExpertHeader);
@@ -1037,11 +1076,16 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
     const int out_dtype = f32 ? MO_F32 : MO_BF16;
     const int64_t ldo = split ? ld_part : q.ldo, stride_o = split ? q.n * ld_part : q.stride_o;
     ExpertArgs p;
-    const int64_t features = plan.pair ? 2 * kBM : kBM, tk = op_ceil_div(q.k, kBN);
+    const int64_t features = shape_features(plan.shape), tk = op_ceil_div(q.k, kBN);
+    // a group's rows take at most 40 MB of L2 (groups of 8 tiles, 16 MB at 4096 columns,
+    // read the weights of an expert with 15 tiles twice: 16384 rows over 8 ragged
+    // experts of 11008 x 4096 923 us)
+    p.group = static_cast<int32_t>(std::max<int64_t>(4, std::min<int64_t>(64, (40 << 20) / (kBN * 2 * depth))));
     p.f_tiles = static_cast<int32_t>(op_ceil_div(mode == kWgrad ? q.n : cols, features));
-    p.width = static_cast<int32_t>(op_ceil_div(op_ceil_div(q.k, tk), 32) * 32);     // equal tiles of at most kBN columns
+    // equal tiles of at most kBN columns, in whole store blocks (a block that reached past its tile would overwrite the next one)
+    p.width = static_cast<int32_t>(op_ceil_div(op_ceil_div(q.k, tk), 64) * 64);
     p.c_tiles = static_cast<int32_t>(op_ceil_div(q.k, p.width));
-    const int64_t tiles = most_tiles(mode, q.rows, q.n, q.k, q.experts, plan.pair) * plan.splits;
+    const int64_t tiles = most_tiles(mode, q.rows, q.n, q.k, q.experts, plan.shape) * plan.splits;
     if (tiles > INT32_MAX) return MO_ERR_UNSUPPORTED;
     bool ok;
     constexpr auto k128 = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -1049,14 +1093,18 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
         ok = encode(&p.a, q.a, MO_BF16, q.n, q.rows, 1, q.lda, 0, 2, 64, 64, k128) &&
              encode(&p.b[0], q.b, MO_BF16, q.k, q.rows, 1, q.ldb, 0, 2, 64, 64, k128) &&
              encode(&p.o, out, out_dtype, q.k, q.n, static_cast<int64_t>(q.experts) * plan.splits, ldo, stride_o, 3,
-                    f32 ? 16 : 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+                    (pair ? 64 : 128) / (f32 ? 4 : 2), 32, pair ? CU_TENSOR_MAP_SWIZZLE_64B : k128);
         for (int i = 1; i < kBoxes; ++i) p.b[i] = p.b[0];
     } else {
         ok = encode(&p.a, q.b, MO_BF16, q.k, q.n, q.experts, q.ldb, q.stride_b, 3, 64, mode == kFwd ? 128 : 64, k128) &&
              encode(&p.o, out, out_dtype, cols, q.rows * plan.splits, 1, ldo, 0, 2, 32, f32 ? 16 : 32,
                     CU_TENSOR_MAP_SWIZZLE_NONE);
-        for (int i = 0; i < kBoxes; ++i)
-            ok = ok && encode(&p.b[i], q.a, MO_BF16, depth, q.rows, 1, q.lda, 0, 2, 64, 128 >> i, k128);
+        for (int i = kBoxes - 1; i >= 0; --i) {         // (boxes that no tile of these rows or this shape takes: not encoded)
+            if ((128 >> i) > shape_columns(plan.shape) || ((128 >> i) >= 32 && (128 >> i) >= 2 * q.rows))
+                p.b[i] = p.b[i + 1];
+            else
+                ok = ok && encode(&p.b[i], q.a, MO_BF16, depth, q.rows, 1, q.lda, 0, 2, 64, 128 >> i, k128);
+        }
     }
     if (!ok) return MO_ERR_UNSUPPORTED;                 // a stride past what a tensor map holds (2^40 bytes)
     p.offsets = q.offsets;
@@ -1067,13 +1115,18 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
     p.n = static_cast<int32_t>(q.n);
     p.k = static_cast<int32_t>(q.k);
     p.experts = q.experts;
-    p.out_f32 = f32;
-    p.accumulate = split ? 0 : q.accumulate;
     p.splits = plan.splits;
     p.chunk = f32 ? kF32Chunk : 1 << 26;                 // more blocks than any sum has
     p.err = static_cast<int*>(ws);
     return op_status(op_traced(MO_K_EXPERT + mode, s, [&] {
-        const cudaError_t e = plan.pair ? launch_mode<true>(mode, f32, p, tiles, s) : launch_mode<false>(mode, f32, p, tiles, s);
+        const bool acc = !split && q.accumulate;        // (split: the join adds)
+        cudaError_t e;
+        if (mode == kWgrad)
+            e = pair ? launch_wgrad<kPairs>(f32, acc, p, tiles, s) : launch_wgrad<kSingle>(f32, acc, p, tiles, s);
+        else
+            e = pair                   ? launch_product<kPairs>(mode, f32, p, tiles, s)
+                : plan.shape == kFew ? launch_product<kFew>(mode, f32, p, tiles, s)
+                                       : launch_product<kSingle>(mode, f32, p, tiles, s);
         if (e != cudaSuccess || !split) return e;
         JoinArgs j;
         j.part = parts;
@@ -1101,9 +1154,9 @@ using namespace mo;
 
 extern "C" {
 
-int mo_debug_set_expert_pair(int on) {
-    if (on < -1 || on > 1) return MO_ERR_INVALID_ARG;
-    return g_expert_pair.exchange(on) + 1;
+int mo_debug_set_expert_shape(int shape) {
+    if (shape < -1 || shape > kFew) return MO_ERR_INVALID_ARG;
+    return g_expert_shape.exchange(shape) + 1;
 }
 
 int expert_linear_workspace_bytes(int64_t rows, int64_t n, int64_t k, int experts, size_t* bytes_out) {

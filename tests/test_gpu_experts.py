@@ -16,12 +16,12 @@ from tests.gpu_helpers import dev
 pytestmark = pytest.mark.gpu
 
 
-@pytest.fixture(params=[-1, 0, 1], ids=["auto", "single", "pair"], autouse=True)
+@pytest.fixture(params=[-1, 0, 1, 2], ids=["auto", "single", "pair", "few"], autouse=True)
 def geometry(request):
-    """Every test runs with the size-chosen tile geometry and with each of the two."""
-    prev = B.mo_debug_set_expert_pair(request.param)
+    """Every test runs with the size-chosen tile geometry and with each of the others."""
+    prev = B.mo_debug_set_expert_shape(request.param)
     yield request.param
-    B.mo_debug_set_expert_pair(prev)
+    B.mo_debug_set_expert_shape(prev)
 
 F32, BF16 = torch.float32, torch.bfloat16
 U = {F32: 2.0 ** -24, BF16: 2.0 ** -8}
