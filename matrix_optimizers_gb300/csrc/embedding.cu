@@ -380,6 +380,41 @@ cudaError_t launch_cluster_sort(const void* ids, int id_dtype, int64_t n, int64_
     return cudaLaunchKernelEx(&cfg, kernel, ids, id_dtype, static_cast<int>(n), vocab, (bits + 1) / 2, keys, pos);
 }
 
+// Up to 2 K positions: a position's place is the number of smaller keys, plus the
+// equal ones before it, counted against every key by eight lanes; any number of
+// blocks can do that side by side.
+constexpr int kRankThreads = 1024, kRankLanes = 8, kRankKeys = kRankThreads / kRankLanes;   // keys ranked by a block
+constexpr int kRankSortMax = 2048;
+
+__global__ void __launch_bounds__(kRankThreads)
+rank_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, uint32_t* keys_out, uint32_t* pos_out) {
+    __shared__ __align__(16) uint32_t key[kRankSortMax];
+    launch_dependents();
+#pragma unroll
+    for (int r = 0; r < kRankSortMax / kRankThreads; ++r) {
+        const int i = r * kRankThreads + static_cast<int>(threadIdx.x);
+        const int64_t id = i < n ? load_id(ids, id_dtype, i, vocab) : -1;
+        key[i] = i >= n ? 0xffffffffu : static_cast<uint32_t>(id < 0 ? vocab : id);   // past the end: above every key
+    }
+    __syncthreads();
+    const int i = static_cast<int>(blockIdx.x) * kRankKeys + static_cast<int>(threadIdx.x) / kRankLanes;
+    const int sub = static_cast<int>(threadIdx.x) % kRankLanes;
+    const uint32_t mine = key[i < n ? i : 0];
+    uint32_t rank = 0;
+#pragma unroll 4
+    for (int j = sub * 4; j < n; j += kRankLanes * 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(key + j);
+        rank += (k.x < mine || (k.x == mine && j < i)) + (k.y < mine || (k.y == mine && j + 1 < i)) +
+                (k.z < mine || (k.z == mine && j + 2 < i)) + (k.w < mine || (k.w == mine && j + 3 < i));
+    }
+#pragma unroll
+    for (int o = kRankLanes / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    if (sub == 0 && i < n) {
+        keys_out[rank] = mine;
+        pos_out[rank] = static_cast<uint32_t>(i);
+    }
+}
+
 // -------------------------------------------------------- sums of sorted runs
 constexpr int kMaxChunk = 64;         // sorted positions per block, at most
 constexpr int kGradThreads = 128;     // columns per block: 128 x one 16-byte access
@@ -692,6 +727,11 @@ int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t
     uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(base + L.pos[0]), reinterpret_cast<uint32_t*>(base + L.pos[1])};
     if (n > 0) {
         const cudaError_t e = op_traced(MO_K_EMBED_SORT, s, [&] {
+            if (n <= kRankSortMax) {
+                rank_sort_kernel<<<static_cast<unsigned>(op_ceil_div(n, kRankKeys)), kRankThreads, 0, s>>>(
+                    ids, id_dtype, static_cast<int>(n), vocab, keys[(L.passes + 1) & 1], pos[(L.passes + 1) & 1]);
+                return cudaGetLastError();
+            }
             if (n <= kClusterSortMax && vocab <= kClusterVocabMax)
                 return launch_cluster_sort<1>(ids, id_dtype, n, vocab, keys[(L.passes + 1) & 1], pos[(L.passes + 1) & 1], s);
             for (int k = 0; k < L.passes; ++k) {
