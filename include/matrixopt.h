@@ -2,7 +2,9 @@
  * matrixopt.h -- C ABI of a GB300 (sm_103a) library for the optimizer step one
  * owner GPU executes for full 2D weight matrices: Muon (momentum, quintic
  * Newton-Schulz orthogonalisation, scaled update), the Sign-Muon sign / 1-bit
- * pack / majority-vote update, AdamW on the 1D tail, and the owner planner.
+ * pack / majority-vote update, AdamW on the 1D tail, and the owner planner;
+ * and operators of the training step around it that make the gradients:
+ * embedding, expert products, distillation from a teacher's top logits.
  *
  * Sources of the operations (web pages on matrix optimizers):
  *   "Riassunto Tecnico: MatrixFSDP" (gist.science/it/paper/2607.05895)
