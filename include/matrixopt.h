@@ -282,7 +282,8 @@ int plan_owners(const int64_t* rows, const int64_t* cols, int n, int world, int 
  * Operators of the training step around the optimizer: they make the
  * gradients that muon_step_batched and the AdamW tail consume.  Matrices are
  * row-major with a leading dimension in elements, as above; element
- * alignment suffices unless an entry says otherwise.  All sums are float32.
+ * alignment suffices unless an entry says otherwise.  Outputs must not overlap
+ * inputs unless an entry says so.  All sums are float32.
  * ------------------------------------------------------------------------ */
 
 /* Embedding lookup: out[i, :] = scale * W[ids[i], :] for i < n, W vocab x dim

@@ -421,8 +421,8 @@ def _matrix(t, what):
     (rows, cols), (ld, unit) = t.shape, t.stride()
     if cols > 1 and unit != 1:
         _invalid(f"{what} must have unit column stride")
-    if rows <= 1 or ld < cols and cols <= 1:
-        ld = max(ld, cols)
+    if rows <= 1:
+        ld = (max(ld, cols) + 7) // 8 * 8          # of a single row nothing depends on it: any aligned value
     code = _DTYPES.get(t.dtype)
     if code is None:
         _invalid(f"{what}: unsupported dtype {t.dtype}")
@@ -492,9 +492,9 @@ def _stack(t, what):
     if cols > 1 and unit != 1:
         _invalid(f"{what} must have unit column stride")
     if rows <= 1:
-        ld = max(ld, cols)
+        ld = (max(ld, cols) + 7) // 8 * 8
     if experts <= 1:
-        stride = max(stride, rows * ld)
+        stride = rows * ld
     code = _DTYPES.get(t.dtype)
     if code is None:
         _invalid(f"{what}: unsupported dtype {t.dtype}")

@@ -11,7 +11,7 @@
 // writes them once.  Loss and gradient in one call read them twice, but the second
 // time from L2: a cluster of CTAs shares a row, so that the rows at work on the
 // device (about 230 of 256 KB at 64 KB per CTA) stay there.  Measured for 8192 rows
-// of 128000 bf16 (4.2 GB at least): 687 us and 4.1 GB of DRAM traffic; with one CTA
+// of 128000 bf16 (4.2 GB at least): 698 us and 4.1 GB of DRAM traffic; with one CTA
 // per row 917 us and 6.3 GB; without the L2 prefetch below 748 us; 32 KB per CTA
 // 916 us and 128 KB 958 us.  Rows kept in shared memory (one read, no L2) were slower,
 // 1020 us with a kernel per row and 1170 us with rows streamed through a persistent
@@ -313,13 +313,15 @@ __device__ __forceinline__ MaxSum join_parts(const MaxSum* part, int ctas, float
 
 // A cluster of 1 to 8 CTAs works on a row, a slice of its 16-byte pieces each;
 // the slices' parts meet through distributed shared memory, joined in rank order.
-template <typename S, typename G, bool kLoss, bool kGrad>
+template <typename S, typename G, bool kLoss, bool kGrad, bool kSplit>
 __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_constant__ DistillArgs a, int slice) {
     extern __shared__ float words[];
     __shared__ float red[kRowWarps + 1];
     __shared__ MaxSum part[kMaxCluster];
     cg::cluster_group cluster = cg::this_cluster();
-    const int ctas = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int ctas = kSplit ? static_cast<int>(cluster.num_blocks()) : 1;
+    const int rank = kSplit ? static_cast<int>(cluster.block_rank()) : 0;
+    if (kSplit) cluster.barrier_arrive();              // (waited for before anything reaches another CTA)
     const int top = a.d.top, V = static_cast<int>(a.d.vocab);
     const Teacher t = {reinterpret_cast<int*>(words), words + top, words + 2 * top, red};
     const int64_t row = blockIdx.x / ctas;
@@ -339,6 +341,7 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
     }
     const bool live = w != 0.f && load_teacher(a, row, t);                       // the same in every CTA of the cluster
     if (!live) {
+        if (kSplit) cluster.barrier_wait();
         if (kLoss && rank == 0 && threadIdx.x == 0) {
             a.loss[row] = 0.f;
             put_stats(a, row, MaxSum{0.f, 1.f});
@@ -364,7 +367,8 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
             add_pieces<S>(ms, raw, a.c);
         }
         st = block_join(ms, a.c, red);
-        if (ctas > 1) {
+        if (kSplit) {
+            cluster.barrier_wait();                    // every CTA has started
             if (static_cast<int>(threadIdx.x) < ctas) *cluster.map_shared_rank(&part[rank], threadIdx.x) = st;
             cluster.sync();                            // the parts are here; every x of the row is read
             st = join_parts(part, ctas, a.c);
@@ -378,6 +382,10 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
         }
     } else {
         st = get_stats(a, row);
+        if (kSplit) {
+            cluster.barrier_wait();
+            cluster.sync();                            // dlogits may be the logits: every x of the row is read
+        }
     }
     if (kGrad) {
         const float inv = st.z == 0.f ? 0.f : 1.f / st.z;
@@ -409,19 +417,25 @@ __global__ void __launch_bounds__(kRowThreads) distill_row_kernel(const __grid_c
 
 template <typename S, typename G, bool kLoss, bool kGrad>
 cudaError_t launch_rows(const DistillArgs& a, int64_t ctas, cudaStream_t s) {
-    const int64_t pieces = op_ceil_div(a.d.vocab, Elem<S>::kVec);
+    const int slice = static_cast<int>(op_ceil_div(op_ceil_div(a.d.vocab, Elem<S>::kVec), ctas));
+    const unsigned grid = static_cast<unsigned>(a.d.n * ctas);
+    const size_t smem = static_cast<size_t>(a.d.top) * 12;
+    if (ctas == 1) {
+        distill_row_kernel<S, G, kLoss, kGrad, false><<<grid, kRowThreads, smem, s>>>(a, slice);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = static_cast<unsigned>(ctas);
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.gridDim = dim3(static_cast<unsigned>(a.d.n * ctas));
+    cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kRowThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.d.top) * 12;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, distill_row_kernel<S, G, kLoss, kGrad>, a, static_cast<int>(op_ceil_div(pieces, ctas)));
+    return cudaLaunchKernelEx(&cfg, distill_row_kernel<S, G, kLoss, kGrad, true>, a, slice);
 }
 
 template <typename S, typename G>
@@ -433,8 +447,7 @@ cudaError_t launch_distill(const DistillArgs& a, bool loss, bool grad, cudaStrea
     if (loss && grad) ctas = std::max<int64_t>(1, std::min<int64_t>(kMaxCluster, op_ceil_div(bytes, kSliceBytes)));
     // few rows: more CTAs each, down to 8 KB, so that every SM has some (8 rows of
     // 32000 bf16: 8 CTAs each 9 us, one each 12 us)
-    if (loss)
-        while (ctas * 2 <= kMaxCluster && a.d.n * ctas * 2 <= device_sm_count() && bytes > ctas * 8192) ctas *= 2;
+    while (ctas * 2 <= kMaxCluster && a.d.n * ctas * 2 <= device_sm_count() && bytes > ctas * 8192) ctas *= 2;
     if (!loss) return launch_rows<S, G, false, true>(a, ctas, s);
     return grad ? launch_rows<S, G, true, true>(a, ctas, s) : launch_rows<S, G, true, false>(a, ctas, s);
 }

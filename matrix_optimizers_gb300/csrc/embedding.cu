@@ -738,8 +738,12 @@ int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t
                     ids, id_dtype, static_cast<int>(n), vocab, keys[(L.passes + 1) & 1], pos[(L.passes + 1) & 1]);
                 return cudaGetLastError();
             }
-            if (n <= kClusterSortMax && vocab <= kClusterVocabMax)
-                return launch_cluster_sort<1>(ids, id_dtype, n, vocab, keys[(L.passes + 1) & 1], pos[(L.passes + 1) & 1], s);
+            if (n <= kClusterSortMax && vocab <= kClusterVocabMax) {
+                const cudaError_t e = launch_cluster_sort<1>(ids, id_dtype, n, vocab, keys[(L.passes + 1) & 1],
+                                                             pos[(L.passes + 1) & 1], s);
+                if (e == cudaSuccess) return e;
+                (void)cudaGetLastError();              // no room for such a cluster (a part of a GPU): the passes below
+            }
             for (int k = 0; k < L.passes; ++k) {
                 SortPass p;
                 p.ids = ids;

@@ -165,3 +165,18 @@ def test_gradient_feeds_the_adamw_tail():
     want = W.double() - 1e-2 * g.double() / (g.double().abs() + 1e-8)      # AdamW's first step
     mo.muon_step_batched([], mo.make_cfg(), None, tail=mo.make_tail(W, g, m, v, 1, lr=1e-2))
     assert torch.allclose(W.double(), want, atol=1e-6)
+
+
+def test_single_rows_and_refused_layouts():
+    W, out = torch.randn((1, 13), device=dev()), torch.empty((1, 13), device=dev())
+    mo.embedding_lookup(W, torch.zeros(1, dtype=torch.int64, device=dev()), out, scale=2.0)
+    assert torch.equal(out, 2 * W)
+    ids = torch.zeros(4, dtype=torch.int64, device=dev())
+    ws = torch.empty(mo.embedding_grad_workspace_bytes(4, 1, 13), dtype=torch.uint8, device=dev())
+    for bad in (out.expand(4, 13), torch.zeros((13, 4), device=dev()).T):
+        with pytest.raises(mo.MoError):
+            mo.embedding_lookup(W, ids, bad)
+        with pytest.raises(mo.MoError):
+            mo.embedding_grad(bad, ids, W, ws)
+    with pytest.raises(mo.MoError):
+        mo.embedding_lookup(W, ids[::2], torch.empty((2, 13), device=dev()))

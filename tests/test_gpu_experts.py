@@ -243,6 +243,26 @@ def test_long_sums_with_few_tiles_are_split_and_joined(sizes, before, after, n, 
     assert mo.mo_check_device_status(ws) == 0
 
 
+def test_a_single_row_of_any_width_and_refused_layouts():
+    """One row needs no aligned pitch; a broadcast or misaligned matrix is refused, not misread."""
+    rng = np.random.default_rng(12)
+    W = _stack(rng, 1, 77, 201)
+    X, Y = torch.randn((1, 201), device=dev()).to(BF16), torch.empty((1, 77), device=dev())
+    o, ws = torch.tensor([0, 1], dtype=torch.int32, device=dev()), _ws(1, 77, 201, 1)
+    mo.expert_linear(X, W, o, Y, ws)
+    _assert_close(Y, ot.expert_linear(_f64(X), _f64(W), [0, 1]),
+                  ot.expert_linear(np.abs(_f64(X)), np.abs(_f64(W)), [0, 1]), 201)
+    o4, Y4 = torch.tensor([0, 4], dtype=torch.int32, device=dev()), torch.empty((4, 80), device=dev())[:, :77]
+    for bad, status in ((X.expand(4, 201), B.MO_ERR_INVALID_ARG), (torch.zeros((4, 201), device=dev(), dtype=BF16),
+                                                                   B.MO_ERR_ALIGNMENT),
+                        (torch.zeros((4, 208), device=dev(), dtype=BF16)[:, 1:202], B.MO_ERR_ALIGNMENT),
+                        (torch.zeros((201, 4), device=dev(), dtype=BF16).T, B.MO_ERR_INVALID_ARG),
+                        (torch.zeros((4, 208), device=dev())[:, :201], B.MO_ERR_INVALID_ARG)):
+        with pytest.raises(B.MoError) as e:
+            mo.expert_linear(bad, W, o4, Y4, ws)
+        assert e.value.status == status
+
+
 @pytest.mark.slow
 def test_large_sizes_against_float64_on_the_device():
     """Long groups, many tiles: sampled rows and columns."""
