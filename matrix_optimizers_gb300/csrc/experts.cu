@@ -814,7 +814,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ JoinA
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (r >= r0 && r < r1)
             for (int s = 0; s < p.splits; ++s) {
-                const float4 x = __ldg(reinterpret_cast<const float4*>(p.part + (s * p.rows + r) * p.ld + c));
+                // (an ordinary load: this kernel may start before the parts are written)
+                const float4 x = *reinterpret_cast<const float4*>(p.part + (s * p.rows + r) * p.ld + c);
                 v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
             }
 #pragma unroll
