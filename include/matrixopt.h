@@ -360,7 +360,7 @@ int expert_linear_wgrad(const void* dY, int64_t ldy, const void* X, int64_t ldx,
  *   distill_topk_loss_grad  both in one pass over the logits
  * dlogits is n x vocab, float32 or bf16, ldg >= vocab; it may be the logits
  * themselves (same type and ld).  1 <= top <= 1024 (MO_ERR_UNSUPPORTED
- * above), vocab < 2^31.  n == 0 is a no-op. */
+ * above), vocab < 2^31 - 1024, T a normal float32.  n == 0 is a no-op. */
 typedef struct {
     int64_t n, vocab, ldl;
     int32_t top, logits_dtype, idx_dtype, teacher_dtype;

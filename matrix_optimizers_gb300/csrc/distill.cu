@@ -32,6 +32,7 @@ namespace cg = cooperative_groups;
 namespace {
 
 constexpr int kMaxTop = 1024;
+constexpr int64_t kMaxVocab = INT32_MAX - 1024;       // a thread's next column, one stride past the last, still fits an int
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kRowAhead = 4;                          // 16-byte pieces in flight per thread
 constexpr int kMaxCluster = 8;
@@ -457,8 +458,8 @@ int check_distill(const mo_distill* d, bool* none) {
     if (d == nullptr) return MO_ERR_INVALID_ARG;
     *none = false;
     if (d->n < 0 || d->vocab < 0 || d->top < 1 || !op_valid_dtype(d->logits_dtype) ||
-        !op_valid_dtype(d->teacher_dtype) || !op_valid_id_dtype(d->idx_dtype) || !(d->temperature > 0.f) ||
-        d->temperature > FLT_MAX)
+        !op_valid_dtype(d->teacher_dtype) || !op_valid_id_dtype(d->idx_dtype) ||
+        !(d->temperature >= FLT_MIN && d->temperature <= FLT_MAX))    // (log2(e) / T overflows for smaller ones)
         return MO_ERR_INVALID_ARG;
     if (d->n == 0) {
         *none = true;
@@ -466,7 +467,7 @@ int check_distill(const mo_distill* d, bool* none) {
     }
     if ((d->vocab > 0 && d->logits == nullptr) || d->idx == nullptr || d->teacher == nullptr || d->ldl < d->vocab)
         return MO_ERR_INVALID_ARG;
-    if (d->top > kMaxTop || d->vocab > INT32_MAX || d->n > INT32_MAX / kMaxCluster) return MO_ERR_UNSUPPORTED;
+    if (d->top > kMaxTop || d->vocab > kMaxVocab || d->n > INT32_MAX / kMaxCluster) return MO_ERR_UNSUPPORTED;
     if (!op_aligned(d->logits, op_elem_size(d->logits_dtype)) || !op_aligned(d->teacher, op_elem_size(d->teacher_dtype)) ||
         !op_aligned(d->idx, op_id_size(d->idx_dtype)) || !op_aligned(d->row_weight, 4))
         return MO_ERR_ALIGNMENT;

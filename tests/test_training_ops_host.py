@@ -130,3 +130,13 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         with pytest.raises(B.MoError) as e:
             call()
         assert e.value.status == B.MO_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("which", ["loss", "grad", "both"])
+def test_distill_refuses_what_its_arithmetic_cannot_hold(lib, which):
+    # a thread's column index, one stride of 256 past the last column, must fit 31 bits
+    for vocab in ((1 << 31) - 1, (1 << 31) - 256):
+        assert dist(lib, which, vocab=vocab, ldl=vocab, ldg=vocab) == B.MO_ERR_UNSUPPORTED, vocab
+    # log2(e) / T must be finite
+    for T in (1e-45, 1e-39):
+        assert dist(lib, which, T=T) == B.MO_ERR_INVALID_ARG, T
