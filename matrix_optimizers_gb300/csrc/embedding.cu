@@ -11,7 +11,8 @@
 // in chunks of kChunk positions: a chunk's threads walk its positions, each
 // thread holding 16 bytes of columns, and write a token's row when its run
 // ends inside the chunk.  A run that crosses chunks leaves float32 partial
-// rows, which the block of the chunk where the run starts adds up in order.
+// rows, counted as they arrive; the block that brings the last one adds them all up,
+// in the chunks' order.
 // Equal chunks keep the work balanced when a few tokens make up most of a batch,
 // as they do in text.
 #include <cooperative_groups.h>
@@ -30,17 +31,6 @@ namespace {
 
 // ------------------------------------------------------------------- lookup
 constexpr int kLookupThreads = 256;
-
-// The 16 bytes at p (a full access), of which `valid` elements are real, as the elements' own bits.
-template <bool kWide, typename W>
-__device__ __forceinline__ uint4 load_piece(const W* p, int valid) {
-    constexpr int V = Elem<W>::kVec;
-    if (kWide && valid >= V) return __ldg(reinterpret_cast<const uint4*>(p));
-    float v[V];
-#pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = k < valid ? Elem<W>::to_float(p[k]) : 0.f;
-    return pack16(v);
-}
 
 // Eight columns per thread and step, so that a bf16 result leaves in 16-byte
 // stores.  A row belongs to 2^row_bits consecutive threads (as many as it has
@@ -110,7 +100,16 @@ cudaError_t launch_lookup(const void* w, int64_t vocab, int64_t dim, int64_t ldw
 constexpr int kDigitBits = 9, kDigits = 1 << kDigitBits;
 constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
 
+// Every sort also clears the sums' arrival counters (its last step before them in the stream).
+__device__ __forceinline__ void clear_counters(uint32_t* arrived, int64_t count) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < count;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
+        arrived[i] = 0;
+}
+
 struct SortPass {
+    uint32_t* arrived;         // the first pass clears these
+    int64_t arrived_count;
     const void* ids;           // the first pass reads the ids, later ones keys_in / pos_in
     int id_dtype;
     const uint32_t* keys_in;
@@ -145,6 +144,7 @@ __device__ __forceinline__ uint32_t sort_key(const SortPass& p, int64_t i) {
 // 32 at a time, so that position order is warp order, then round, then lane.
 __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const __grid_constant__ SortPass p) {
     __shared__ uint32_t hist[kDigits];
+    if (p.keys_in == nullptr) clear_counters(p.arrived, p.arrived_count);
     for (int d = threadIdx.x; d < p.digits; d += kSortThreads) hist[d] = 0;
     __syncthreads();
     const int64_t tile0 = static_cast<int64_t>(blockIdx.x) * p.rounds * kSortThreads;
@@ -247,8 +247,9 @@ static_assert(sizeof(ClusterSmem) <= 232448, "shared memory");
 template <int kRounds>
 __global__ void __launch_bounds__(kClusterThreads, 1)
 cluster_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, int digit_bits, uint32_t* keys_out,
-                    uint32_t* pos_out) {
+                    uint32_t* pos_out, uint32_t* arrived, int64_t arrived_count) {
     launch_dependents();
+    clear_counters(arrived, arrived_count);
     extern __shared__ __align__(16) uint8_t smem_raw[];
     ClusterSmem& sm = *reinterpret_cast<ClusterSmem*>(smem_raw);
     cg::cluster_group cluster = cg::this_cluster();
@@ -347,10 +348,11 @@ cluster_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, int dig
 
 template <int kRounds>
 cudaError_t launch_cluster_sort(const void* ids, int id_dtype, int64_t n, int64_t vocab, uint32_t* keys, uint32_t* pos,
-                                cudaStream_t s) {
+                                uint32_t* arrived, int64_t arrived_count, cudaStream_t s) {
     // spread over the cluster first, then over rounds
     if (kRounds < kClusterRounds && n > static_cast<int64_t>(kClusterMax) * kRounds * kClusterThreads)
-        return launch_cluster_sort<kRounds < kClusterRounds ? 2 * kRounds : kRounds>(ids, id_dtype, n, vocab, keys, pos, s);
+        return launch_cluster_sort<kRounds < kClusterRounds ? 2 * kRounds : kRounds>(ids, id_dtype, n, vocab, keys, pos, arrived,
+                                                                                           arrived_count, s);
     static std::atomic<uint64_t> attr_set{0};        // one bit per device ordinal
     const auto kernel = cluster_sort_kernel<kRounds>;
     int dev = 0;
@@ -378,7 +380,8 @@ cudaError_t launch_cluster_sort(const void* ids, int id_dtype, int64_t n, int64_
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, ids, id_dtype, static_cast<int>(n), vocab, (bits + 1) / 2, keys, pos);
+    return cudaLaunchKernelEx(&cfg, kernel, ids, id_dtype, static_cast<int>(n), vocab, (bits + 1) / 2, keys, pos, arrived,
+                              arrived_count);
 }
 
 // Up to 2 K positions: a position's place is the number of smaller keys, plus the
@@ -388,9 +391,11 @@ constexpr int kRankThreads = 1024, kRankLanes = 8, kRankKeys = kRankThreads / kR
 constexpr int kRankSortMax = 2048;
 
 __global__ void __launch_bounds__(kRankThreads)
-rank_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, uint32_t* keys_out, uint32_t* pos_out) {
+rank_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, uint32_t* keys_out, uint32_t* pos_out,
+                 uint32_t* arrived, int64_t arrived_count) {
     __shared__ __align__(16) uint32_t key[kRankSortMax];
     launch_dependents();
+    clear_counters(arrived, arrived_count);
 #pragma unroll
     for (int r = 0; r < kRankSortMax / kRankThreads; ++r) {
         const int i = r * kRankThreads + static_cast<int>(threadIdx.x);
@@ -417,11 +422,15 @@ rank_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, uint32_t* 
 }
 
 // -------------------------------------------------------- sums of sorted runs
-// Bound by the table's write: 128000 x 2048 float32 from 32768 bf16 rows 173 us, 81%
-// of the DRAM's peak (207 us with the loaded rows unpacked ahead of their use: 89
-// registers instead of 56, fewer blocks per SM).  A separate kernel that zeroes absent
+// Bound by the table's write: 128000 x 2048 float32 from 32768 bf16 rows 191 us a call, 174
+// of them the bytes at the rate of a copy; the sort takes 17.  A kernel of its own
+// for the runs that cross chunks took 201 us, and 335 against 205 us where 8192 positions
+// hold one token (1024 columns, 32000 rows).  A separate kernel that zeroes absent
 // rows beside the sort gained nothing (204 us a call against 202), one that zeroes all
-// of them lost 50 us: the fill hides the sums' latency.
+// of them lost 50 us: the fill hides the sums' latency.  Up to 1024 positions without a
+// sort, each block searching the ids for its token's, was faster only without a fill
+// (777 x 1024: 10 us against 15) and slower otherwise (777 x 515 into 5003 rows 18 us
+// against 14, one token alone 41 us against 21).
 constexpr int kMaxChunk = 64;         // sorted positions per block, at most
 constexpr int kGradThreads = 128;     // columns per block: 128 x one 16-byte access
 constexpr int kMaxZeroRows = 64;      // table rows per block of the zero fill, at most
@@ -437,7 +446,9 @@ struct GradArgs {
     const uint32_t* pos;
     void* dw;
     int64_t ldw;
-    float* part;                      // [chunk][2][dim]: a run's rows in a chunk it enters from before, or leaves
+    float* part;                      // [chunk][2][part_ld]: a run's rows in a chunk it enters from before, or leaves
+    int64_t part_ld;                  // dim up to whole pieces
+    uint32_t* arrived;                // [chunk][column slab]: parts there of the run that leaves that chunk
     float scale;
     int accumulate, wide_out;
     int chunk, zero_rows;             // positions per chunk, table rows per zero-fill block
@@ -461,6 +472,16 @@ __device__ __forceinline__ void write_row(const GradArgs& a, uint32_t key, int64
         for (int k = 0; k < V; ++k)
             if (k < nv) dst[k] = Elem<D>::from_float(v[k]);
     }
+}
+
+// `valid` elements at p one by one, as the bits of a whole piece.
+template <typename T>
+__device__ __forceinline__ uint4 load_elements(const T* p, int valid) {
+    constexpr int V = Elem<T>::kVec;
+    float v[V];
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = k < valid ? Elem<T>::to_float(p[k]) : 0.f;
+    return pack16(v);
 }
 
 // First sorted position in [lo, hi] whose key is not below v.
@@ -487,9 +508,8 @@ __device__ __forceinline__ int64_t warp_lower_bound_key(const uint32_t* keys, in
 }
 
 template <typename T, typename D, bool kWide>
-__global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_constant__ GradArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 7) grad_sum_kernel(const __grid_constant__ GradArgs a) {
     constexpr int V = Elem<T>::kVec;
-    launch_dependents();
     wait_for_previous();
     if (blockIdx.x >= a.sum_blocks) {                // rows of absent tokens: zeros
         const int64_t r0 = (static_cast<int64_t>(blockIdx.x) - a.sum_blocks) * a.zero_rows;
@@ -527,32 +547,45 @@ __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_con
         return;
     }
     __shared__ uint32_t skey[kMaxChunk + 2], spos[kMaxChunk];   // skey[0], skey[len + 1]: the neighbours' keys
+    __shared__ int last_here[2];
+    __shared__ int64_t span[2][2];
     const int64_t chunk = blockIdx.x % a.chunks, slab = blockIdx.x / a.chunks;
     const int64_t p0 = chunk * a.chunk;
     const int len = static_cast<int>(a.n - p0 < a.chunk ? a.n - p0 : a.chunk);
     const uint32_t none = 0xffffffffu, dropped = static_cast<uint32_t>(a.vocab);
-    for (int i = threadIdx.x; i < len + 2; i += kGradThreads) {
-        const int64_t q = p0 + i - 1;
-        skey[i] = q >= 0 && q < a.n ? a.keys[q] : none;
+    auto key_at = [&](int64_t q) { return q >= 0 && q < a.n ? a.keys[q] : none; };
+    for (int i = threadIdx.x; i < len + 2; i += kGradThreads) skey[i] = key_at(p0 + i - 1);
+    // warp 0: the last keys of the 32 chunks before; warp 1: the first keys of the 32 after
+    uint32_t edge = none;
+    if (threadIdx.x < 64) {
+        const int64_t off = static_cast<int64_t>(threadIdx.x & 31) * a.chunk;
+        edge = key_at(threadIdx.x < 32 ? p0 - 1 - off : p0 + a.chunk + off);
     }
     for (int i = threadIdx.x; i < len; i += kGradThreads) spos[i] = a.pos[p0 + i];
     __syncthreads();
     const int64_t c = (slab * kGradThreads + threadIdx.x) * V;
-    if (c >= a.dim) return;
-    const int nv = static_cast<int>(a.dim - c < V ? a.dim - c : V);
+    const int nv = static_cast<int>(c >= a.dim ? 0 : a.dim - c < V ? a.dim - c : V);   // this thread's columns
     const T* dy = static_cast<const T*>(a.dy) + c;
+    const bool enters = skey[0] == skey[1] && skey[1] != dropped, leaves = skey[len + 1] == skey[len] && skey[len] != dropped;
     float acc[V];
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
-    bool from_before = skey[0] == skey[1];
-    for (int i0 = 0; i0 < len; i0 += kAhead) {
+    bool from_before = enters;
+    for (int i0 = 0; i0 < (nv > 0 ? len : 0); i0 += kAhead) {
         uint4 raw[kAhead];
+        auto load_rows = [&](auto load) {
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + u;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (i < len && skey[i + 1] != dropped) raw[u] = load_piece<kWide>(dy + static_cast<int64_t>(spos[i]) * a.ldy, nv);
-        }
+            for (int u = 0; u < kAhead; ++u) {
+                raw[u] = make_uint4(0, 0, 0, 0);
+                if (i0 + u < len && skey[i0 + u + 1] != dropped)
+                    raw[u] = load(dy + static_cast<int64_t>(spos[i0 + u]) * a.ldy);
+            }
+        };
+        // (two loops: the choice inside one keeps the loads from being issued back to back)
+        if (kWide && nv == V)
+            load_rows([](const T* p) { return __ldg(reinterpret_cast<const uint4*>(p)); });
+        else
+            load_rows([&](const T* p) { return load_elements(p, nv); });
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             const int i = i0 + u;
@@ -566,10 +599,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_con
             const bool goes_on = last && skey[i + 2] == skey[i + 1];
             if (from_before || goes_on) {
                 // slot 0: the run entered from before (and perhaps goes on); slot 1: it starts here and goes on
-                float* dst = a.part + ((chunk * 2 + (from_before ? 0 : 1)) * a.dim + c);
-#pragma unroll
-                for (int k = 0; k < V; ++k)
-                    if (k < nv) dst[k] = acc[k];
+                store_run<float, V>(a.part + ((chunk * 2 + (from_before ? 0 : 1)) * a.part_ld + c), acc, true);
             } else {
                 write_row<D, V>(a, skey[i + 1], c, nv, acc);
             }
@@ -578,44 +608,62 @@ __global__ void __launch_bounds__(kGradThreads) grad_sum_kernel(const __grid_con
             for (int k = 0; k < V; ++k) acc[k] = 0.f;
         }
     }
-}
-
-// The block of a chunk whose last run goes on adds that run's partial rows, in
-// order; the run reaches chunk q when q's first key is still its own.
-constexpr int kJoinThreads = 256;
-template <typename T, typename D>
-__global__ void __launch_bounds__(kJoinThreads) grad_join_kernel(const __grid_constant__ GradArgs a) {
-    wait_for_previous();
-    const int64_t chunk = blockIdx.x, first = chunk * a.chunk, next = first + a.chunk;
-    if (next >= a.n) return;
-    const uint32_t key = a.keys[next - 1], after = a.keys[next], head = a.keys[first];
-    const uint32_t before = a.keys[first > 0 ? first - 1 : 0];
-    if (key == static_cast<uint32_t>(a.vocab) || after != key) return;
-    if (first > 0 && head == key && before == key) return;                     // an earlier chunk's run
-    for (int64_t c = static_cast<int64_t>(blockIdx.y) * kJoinThreads + threadIdx.x; c < a.dim;
-         c += static_cast<int64_t>(gridDim.y) * kJoinThreads) {
-        float acc = a.part[(chunk * 2 + 1) * a.dim + c];
-        for (int64_t q = chunk + 1;; q += kAhead) {
-            float v[kAhead];
-            bool on[kAhead];
+    // A run that crosses chunks: the block that brings its last part adds all of
+    // them, in the chunks' order whichever block that is.
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {                                       // the run that enters, the one that leaves
+        if (side == 0 ? !enters : !leaves || (enters && skey[1] == skey[len])) continue;   // block-uniform
+        const uint32_t key = skey[side == 0 ? 1 : len];
+        // the run's chunks: as many neighbours as end (begin) with its key; more than 32 are searched for
+        const bool from_left = side == 0, to_right = side == 1 || (leaves && skey[len] == key);
+        if (threadIdx.x < 64) {
+            const bool first = threadIdx.x < 32;
+            const uint32_t other = ~__ballot_sync(0xffffffffu, edge == key);
+            const int more = __ffs(other) - 1;                                   // -1: all 32
+            int64_t q = chunk;
+            if (first && from_left)
+                q = more >= 0 ? chunk - more : warp_lower_bound_key(a.keys, a.n, key) / a.chunk;
+            else if (!first && to_right)
+                q = more >= 0 ? chunk + more : (warp_lower_bound_key(a.keys, a.n, static_cast<int64_t>(key) + 1) - 1) / a.chunk;
+            if ((threadIdx.x & 31) == 0) span[side][first ? 0 : 1] = q;
+        }
+        __syncthreads();                                                         // and the block's parts are written
+        const int64_t q0 = span[side][0], q1 = span[side][1];
+        if (threadIdx.x == 0) {
+            __threadfence();
+            last_here[side] = atomicAdd(&a.arrived[q0 * (a.sum_blocks / a.chunks) + slab], 1u) == static_cast<uint32_t>(q1 - q0);
+            __threadfence();
+        }
+        __syncthreads();
+        if (!last_here[side] || nv == 0) continue;
+        constexpr int kRows = 32 / V;                                            // parts in flight per thread
+        const float* src = a.part + c;
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                on[u] = q + u < a.chunks && a.keys[(q + u) * a.chunk] == key;
-                v[u] = q + u < a.chunks ? a.part[(q + u) * 2 * a.dim + c] : 0.f;   // not a run's: unused
+        for (int k = 0; k < V; ++k) acc[k] = 0.f;
+        for (int64_t q = q0; q <= q1; q += kRows) {
+            float v[kRows][V];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const float* row = src + ((q + u) * 2 + (q + u == q0 ? 1 : 0)) * a.part_ld;
+#pragma unroll
+                for (int k = 0; k < V; k += 4) {
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (q + u <= q1) x = __ldcg(reinterpret_cast<const float4*>(row + k));   // from L2, where other blocks' parts are
+                    v[u][k] = x.x; v[u][k + 1] = x.y; v[u][k + 2] = x.z; v[u][k + 3] = x.w;
+                }
             }
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u)
-                if (on[u]) acc += v[u];
-            if (!on[kAhead - 1]) break;
+            for (int u = 0; u < kRows; ++u)
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc[k] += v[u][k];
         }
-        float one[1] = {acc};
-        write_row<D, 1>(a, key, c, 1, one);
+        write_row<D, V>(a, key, c, nv, acc);
     }
 }
 
 struct GradLayout {
-    size_t keys[2], pos[2], counts, part, total;
-    int64_t chunks;
+    size_t keys[2], pos[2], counts, part, arrived, total;
+    int64_t chunks, part_ld, arrived_count;
     int passes, digit_bits, tiles, rounds, chunk;
 };
 
@@ -637,7 +685,10 @@ GradLayout grad_layout(int64_t n, int64_t vocab, int64_t dim) {
     for (int k = 0; k < 2; ++k) L.keys[k] = take(static_cast<size_t>(n) * 4);
     for (int k = 0; k < 2; ++k) L.pos[k] = take(static_cast<size_t>(n) * 4);
     L.counts = take((static_cast<size_t>(L.tiles) << L.digit_bits) * 4);
-    L.part = take(static_cast<size_t>(L.chunks) * 2 * static_cast<size_t>(dim) * 4);
+    L.part_ld = op_ceil_div(dim, 8) * 8;
+    L.part = take(static_cast<size_t>(L.chunks) * 2 * static_cast<size_t>(L.part_ld) * 4);
+    L.arrived_count = L.chunks * op_ceil_div(dim, kGradThreads * 4);    // column slabs, at most
+    L.arrived = take(static_cast<size_t>(L.arrived_count) * 4);
     L.total = o > 256 ? o : 256;
     return L;
 }
@@ -653,18 +704,10 @@ cudaError_t launch_grad(const GradArgs& a0, cudaStream_t s) {
     a.zero_rows = kMaxZeroRows;
     while (a.zero_rows > 4 && op_ceil_div(a.vocab, a.zero_rows) < 4 * kGradBlocks) a.zero_rows /= 2;
     const int64_t zero_blocks = a.accumulate ? 0 : op_ceil_div(a.vocab, a.zero_rows);
-    if (a.sum_blocks + zero_blocks > 0) {
-        const unsigned grid = static_cast<unsigned>(a.sum_blocks + zero_blocks);
-        const cudaError_t e = wide_in ? launch_after(grad_sum_kernel<T, D, true>, grid, kGradThreads, s, a)
-                                      : launch_after(grad_sum_kernel<T, D, false>, grid, kGradThreads, s, a);
-        if (e != cudaSuccess) return e;
-    }
-    if (a.chunks > 1) {
-        const int64_t by = op_ceil_div(a.dim, 2 * kJoinThreads);
-        return launch_after(grad_join_kernel<T, D>,
-                            dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(by < 64 ? by : 64)), kJoinThreads, s, a);
-    }
-    return cudaSuccess;
+    const unsigned grid = static_cast<unsigned>(a.sum_blocks + zero_blocks);
+    if (grid == 0) return cudaSuccess;
+    return wide_in ? launch_after(grad_sum_kernel<T, D, true>, grid, kGradThreads, s, a)
+                   : launch_after(grad_sum_kernel<T, D, false>, grid, kGradThreads, s, a);
 }
 
 constexpr int64_t kMaxCount = (int64_t(1) << 31) - 1;
@@ -731,21 +774,25 @@ int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t
     uint8_t* base = static_cast<uint8_t*>(ws);
     uint32_t* keys[2] = {reinterpret_cast<uint32_t*>(base + L.keys[0]), reinterpret_cast<uint32_t*>(base + L.keys[1])};
     uint32_t* pos[2] = {reinterpret_cast<uint32_t*>(base + L.pos[0]), reinterpret_cast<uint32_t*>(base + L.pos[1])};
+    uint32_t* arrived = reinterpret_cast<uint32_t*>(base + L.arrived);
     if (n > 0) {
         const cudaError_t e = op_traced(MO_K_EMBED_SORT, s, [&] {
             if (n <= kRankSortMax) {
                 rank_sort_kernel<<<static_cast<unsigned>(op_ceil_div(n, kRankKeys)), kRankThreads, 0, s>>>(
-                    ids, id_dtype, static_cast<int>(n), vocab, keys[(L.passes + 1) & 1], pos[(L.passes + 1) & 1]);
+                    ids, id_dtype, static_cast<int>(n), vocab, keys[(L.passes + 1) & 1], pos[(L.passes + 1) & 1], arrived,
+                    L.arrived_count);
                 return cudaGetLastError();
             }
             if (n <= kClusterSortMax && vocab <= kClusterVocabMax) {
                 const cudaError_t e = launch_cluster_sort<1>(ids, id_dtype, n, vocab, keys[(L.passes + 1) & 1],
-                                                             pos[(L.passes + 1) & 1], s);
+                                                             pos[(L.passes + 1) & 1], arrived, L.arrived_count, s);
                 if (e == cudaSuccess) return e;
                 (void)cudaGetLastError();              // no room for such a cluster (a part of a GPU): the passes below
             }
             for (int k = 0; k < L.passes; ++k) {
                 SortPass p;
+                p.arrived = arrived;
+                p.arrived_count = L.arrived_count;
                 p.ids = ids;
                 p.id_dtype = id_dtype;
                 p.keys_in = k == 0 ? nullptr : keys[(k + 1) & 1];
@@ -781,6 +828,8 @@ int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t
     a.dw = dW;
     a.ldw = ldw;
     a.part = reinterpret_cast<float*>(base + L.part);
+    a.part_ld = L.part_ld;
+    a.arrived = arrived;
     a.scale = scale;
     a.accumulate = accumulate;
     a.chunk = L.chunk;

@@ -123,6 +123,26 @@ def test_gradient_is_the_same_bit_for_bit_and_ignores_dropped_rows():
     assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2]) and bool(torch.isfinite(out[0]).all())
 
 
+@pytest.mark.parametrize("vocab", [60, 300000])           # sorted in one launch, in passes
+@pytest.mark.parametrize("dim,dtype", [(20, F32), (1100, BF16), (1031, F32)])
+def test_gradient_of_runs_that_end_at_and_around_chunks(vocab, dim, dtype):
+    """Runs of 1 to 70 chunks whose ends fall on, before and after a chunk's, twice with one workspace."""
+    rng = np.random.default_rng(dim)
+    lengths = [3, 8, 8, 16, 5, 1, 2, 64, 63, 65, 128, 256, 264, 255, 31 * 64, 33 * 64 + 1, 7, 9, 560, 1, 1, 70]
+    ws = None
+    for order in (lengths, lengths[::-1]):
+        ids = np.repeat(np.arange(len(order)), order)
+        rng.shuffle(ids)
+        n = len(ids)
+        dY = _rand(rng, (n, dim), dtype)
+        dW = _rand(rng, (vocab, dim), F32)
+        start = _f64(dW[:64])
+        if ws is None:
+            ws = torch.full((mo.embedding_grad_workspace_bytes(n, vocab, dim),), 255, dtype=torch.uint8, device=dev())
+        mo.embedding_grad(dY, torch.from_numpy(ids).to(dev()), dW, ws, scale=0.5, accumulate=True)
+        _check_grad(dY, ids, min(vocab, 64), dW[:64], 0.5, start)
+
+
 def test_gradient_of_no_positions_is_zero_and_runs_on_another_stream():
     dW = torch.ones((70, 33), device=dev())
     ws = torch.empty(mo.embedding_grad_workspace_bytes(0, 70, 33), dtype=torch.uint8, device=dev())
