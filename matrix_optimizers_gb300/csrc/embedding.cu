@@ -424,7 +424,7 @@ rank_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, uint32_t* 
 // -------------------------------------------------------- sums of sorted runs
 // Bound by the table's write: 128000 x 2048 float32 from 32768 bf16 rows 191 us a call, 174
 // of them the bytes at the rate of a copy; the sort takes 17.  A kernel of its own
-// for the runs that cross chunks took 201 us, and 335 against 205 us where 8192 positions
+// for the runs that cross chunks took 201 us, and 335 against 111 us where 8192 positions
 // hold one token (1024 columns, 32000 rows).  A separate kernel that zeroes absent
 // rows beside the sort gained nothing (204 us a call against 202), one that zeroes all
 // of them lost 50 us: the fill hides the sums' latency.  Up to 1024 positions without a
@@ -436,8 +436,11 @@ constexpr int kGradThreads = 128;     // columns per block: 128 x one 16-byte ac
 constexpr int kMaxZeroRows = 64;      // table rows per block of the zero fill, at most
 constexpr int kAhead = 8;             // rows in flight per thread
 // Chunks halve (down to 8) until the sums have this many blocks: a small batch is
-// bound by the latency of its rows, a large one by their bytes.
-constexpr int64_t kGradBlocks = 600;
+// bound by the latency of its rows, a large one by their bytes, a frequent token's
+// run by its chunks (8192 x 1024, 150 / 300 / 600 blocks: tokens evenly drawn 43 / 39 / 37 us,
+// as in text 42 / 41 / 47, one token alone 63 / 111 / 204).
+constexpr int64_t kGradBlocks = 300;
+constexpr int64_t kZeroBlocks = 2400; // and the zero fill's blocks halve their rows (down to 4) until there are this many
 
 struct GradArgs {
     const void* dy;
@@ -702,7 +705,7 @@ cudaError_t launch_grad(const GradArgs& a0, cudaStream_t s) {
     const int64_t slabs = op_ceil_div(a.dim, static_cast<int64_t>(kGradThreads) * V);
     a.sum_blocks = a.chunks * slabs;
     a.zero_rows = kMaxZeroRows;
-    while (a.zero_rows > 4 && op_ceil_div(a.vocab, a.zero_rows) < 4 * kGradBlocks) a.zero_rows /= 2;
+    while (a.zero_rows > 4 && op_ceil_div(a.vocab, a.zero_rows) < kZeroBlocks) a.zero_rows /= 2;
     const int64_t zero_blocks = a.accumulate ? 0 : op_ceil_div(a.vocab, a.zero_rows);
     const unsigned grid = static_cast<unsigned>(a.sum_blocks + zero_blocks);
     if (grid == 0) return cudaSuccess;
