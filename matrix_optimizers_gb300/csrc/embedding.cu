@@ -384,11 +384,14 @@ cudaError_t launch_cluster_sort(const void* ids, int id_dtype, int64_t n, int64_
                               arrived_count);
 }
 
-// Up to 2 K positions: a position's place is the number of smaller keys, plus the
-// equal ones before it, counted against every key by eight lanes; any number of
-// blocks can do that side by side (777 positions 6 us, the cluster's two passes 9).
-constexpr int kRankThreads = 1024, kRankLanes = 8, kRankKeys = kRankThreads / kRankLanes;   // keys ranked by a block
-constexpr int kRankSortMax = 2048;
+// Up to 4 K positions: a position's place is the number of smaller keys, plus the
+// equal ones before it, counted against every key by a warp; any number of
+// blocks can do that side by side.  The gradient's call (512 columns, 5003 rows) for
+// 777 / 2048 / 4096 positions: 10.7 / 14.7 / 22.8 us, with eight lanes per position and blocks of
+// 1024 threads 13.6 / 20.7 / -, with the cluster's two passes - / - / 23.0 (into 32000 rows 22.8
+// against 26.5; 8192 positions 42 against 25).
+constexpr int kRankThreads = 512, kRankLanes = 32, kRankKeys = kRankThreads / kRankLanes;   // keys ranked by a block
+constexpr int kRankSortMax = 4096;
 
 __global__ void __launch_bounds__(kRankThreads)
 rank_sort_kernel(const void* ids, int id_dtype, int n, int64_t vocab, uint32_t* keys_out, uint32_t* pos_out,

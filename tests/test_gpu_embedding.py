@@ -123,6 +123,18 @@ def test_gradient_is_the_same_bit_for_bit_and_ignores_dropped_rows():
     assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2]) and bool(torch.isfinite(out[0]).all())
 
 
+@pytest.mark.parametrize("n", [31, 32, 33, 511, 513, 2049, 4095, 4096, 4097])
+def test_gradient_at_the_ends_of_the_sorts(n):
+    rng = np.random.default_rng(n)
+    ids = _ids(rng, n, 90, "zipf")
+    ids[rng.random(n) < 0.1] = -1
+    dY = _rand(rng, (n, 12), F32)
+    dW = torch.full((90, 12), float("nan"), device=dev())
+    ws = torch.full((mo.embedding_grad_workspace_bytes(n, 90, 12),), 255, dtype=torch.uint8, device=dev())
+    mo.embedding_grad(dY, torch.from_numpy(ids).to(dev()), dW, ws)
+    _check_grad(dY, ids, 90, dW, 1.0)
+
+
 @pytest.mark.parametrize("vocab", [60, 300000])           # sorted in one launch, in passes
 @pytest.mark.parametrize("dim,dtype", [(20, F32), (1100, BF16), (1031, F32)])
 def test_gradient_of_runs_that_end_at_and_around_chunks(vocab, dim, dtype):
