@@ -11,7 +11,7 @@
 // writes them once.  Loss and gradient in one call read them twice, but the second
 // time from L2: a cluster of CTAs shares a row, so that the rows at work on the
 // device (about 230 of 256 KB at 64 KB per CTA) stay there.  Measured for 8192 rows
-// of 128000 bf16 (4.2 GB at least): 698 us and 4.1 GB of DRAM traffic; with one CTA
+// of 128000 bf16 (4.2 GB at least): 705 us and 4.1 GB of DRAM traffic; with one CTA
 // per row 917 us and 6.3 GB; without the L2 prefetch below 748 us; 32 KB per CTA
 // 916 us and 128 KB 958 us.  Rows kept in shared memory (one read, no L2) were slower,
 // 1020 us with a kernel per row and 1170 us with rows streamed through a persistent
@@ -143,12 +143,16 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
 
 // The exponent of exp((v - m) / T) in base 2, as one fused v c - b with c =
 // log2(e) / T and b = m c rounded: the same b stands in every term of a sum and of a
-// quotient, so that its rounding cancels (rho, what b lacks of m c, appears where the
-// loss needs m itself).  Logits so large that m c is useless or overflows take (v - m) c.
+// quotient, so that its rounding cancels (rho, what b lacks of m c, appears where sums of
+// different shifts meet and where the loss needs m itself).  Each term then carries 2^rho, so
+// this form is taken only while b's last place is at most 1 and |rho| at most 1/2.  Larger
+// products take (v - m) c, whose rounding is relative to the difference: logits near the
+// maximum lose nothing.
+constexpr float kFusedShift = 16777216.f;              // 2^24
 struct Shift {
     float m, c, b;
     bool fused;
-    __device__ Shift(float m_, float c_) : m(m_), c(c_), b(m_ * c_), fused(fabsf(m_ * c_) < 1e30f) {}
+    __device__ Shift(float m_, float c_) : m(m_), c(c_), b(m_ * c_), fused(fabsf(m_ * c_) < kFusedShift) {}
     __device__ float operator()(float v) const { return fused ? fmaf(v, c, -b) : (v - m) * c; }
     __device__ float rho() const { return fused ? fmaf(m, c, -b) : 0.f; }
 };
@@ -159,10 +163,12 @@ struct Shift {
 struct MaxSum {
     float m, z;
 };
-// The factor that takes a sum from maximum `from` to maximum `to` >= from.
+// The factor that takes a sum from maximum `from` to maximum `to` >= from: b minus b,
+// which is (from - to) c - rho(from) + rho(to), the form that also holds where only one
+// is fused (1% of the batch's time: 698 us without it).
 __device__ __forceinline__ float rescale(float from, float to, float c) {
     const Shift x(from, c), y(to, c);
-    return exp2_fast(x.fused && y.fused ? x.b - y.b : (from - to) * c);
+    return exp2_fast(x.fused && y.fused ? x.b - y.b : (from - to) * c - x.rho() + y.rho());
 }
 __device__ __forceinline__ void add_logit(MaxSum& a, float x, float c) {
     const float m = fmaxf(a.m, x);

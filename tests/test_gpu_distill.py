@@ -215,3 +215,63 @@ def test_other_stream():
     mo.distill_topk_loss_grad(s, idx, t, loss, g, stream=st)
     st.synchronize()
     _check(s, idx, t, 1.0, None, 1.0, loss, g)
+
+
+def _wide_range_rows(s, idx, far):
+    """Rows whose largest or smallest logits are `far` away from the ordinary ones, and
+    rows on either side of where float32 logits get sparse."""
+    V = s.size(1)
+    low, high = -far, far
+    s[0, : 3 * V // 4] = low                     # a masked run: threads that see nothing else at first
+    s[1] = low                                   # the whole row: q is uniform
+    s[2, :9] = low                               # what lies before the first, after the last 16-byte boundary
+    s[2, -9:] = low
+    s[3] = low                                   # all but one
+    s[3, V // 2] = 1.0
+    s[4, idx[4, :2].long()] = low                # where the teacher wants them
+    s[5, V // 3] = high                          # one logit far above the others
+    s[6] = high
+    at = torch.arange(V, device=s.device) * 7 % 11
+    s[7] = (3e7 + 2 * at).to(s.dtype)            # neighbouring float32 values
+    s[8] = (-2.4e7 - 2 * at).to(s.dtype)
+    s[8, ::3] = low
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [0.3, 1.0, 2.0, 4.0])
+@pytest.mark.parametrize("far", [1e9, 1e10, 1e12, 1e20])
+@pytest.mark.parametrize("n,V,ld,shift", [(9, 61, 67, 1), (9, 20001, 20010, 3), (320, 2050, None, 0)])
+def test_logits_of_any_size(n, V, ld, shift, far, T, dtype):
+    s, idx, t = _inputs(17, n, V, 6, dtype, ld=ld, shift=shift)
+    _wide_range_rows(s, idx, far)
+    for loss, grad in _run(s, idx, t, T=T, ld=ld, shift=shift):
+        _check(s, idx, t, T, None, 1.0, loss, grad)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [1e-5, 1e-9, 1e-20, 1e-30])
+@pytest.mark.parametrize("n,V,shift", [(64, 50, 1), (8, 20001, 0)])
+def test_low_temperatures(n, V, shift, T, dtype):
+    """The largest logit alone counts, whatever its product with 1/T rounds to.  (Half of
+    the teachers are uniform: their probabilities do not depend on T.)"""
+    s, idx, t = _inputs(18, n, V, 6, dtype, shift=shift)
+    s += 10
+    s[1] = s[1, 0].clone()
+    t[::2] = 1.0
+    for loss, grad in _run(s, idx, t, T=T, shift=shift):
+        _check(s, idx, t, T, None, 1.0, loss, grad)
+
+
+@pytest.mark.parametrize("n", [1, 3])
+def test_statistics_hold_the_maximum_and_the_sum(n):
+    """stats = {max s, sum exp((s - max) / T)} also for a maximum whose product with 1/T rounds coarsely."""
+    s, idx, t = _inputs(19, n, 4000, 5, F32)
+    s[0] = 1e9
+    s[0, :100] = 1e9 - 64
+    for T in (1.0, 64.0, 1e-9):
+        loss, stats = torch.empty(n, device=dev()), torch.empty((n, 2), device=dev())
+        mo.distill_topk_loss(s, idx, t, loss, stats, temperature=T)
+        x = s.double()
+        z = torch.exp((x - x.amax(1, keepdim=True)) / float(np.float32(T))).sum(1)
+        assert torch.equal(stats[:, 0], s.amax(1))
+        assert torch.all((stats[:, 1].double() - z).abs() <= (4000 / 128 + 68) * 2.0 ** -24 * z)
