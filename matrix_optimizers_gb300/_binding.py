@@ -394,6 +394,7 @@ def _call(name):
 
 
 _current_raw_stream = torch._C._cuda_getCurrentRawStream   # current_stream() without building a Stream object
+_current_device = torch._C._cuda_getDevice                 # (a CUDA tensor is at hand: initialised)
 _DTYPES = {torch.float32: MO_F32, torch.bfloat16: MO_BF16}
 _ID_DTYPES = {torch.int32: MO_I32, torch.int64: MO_I64}
 
@@ -403,15 +404,22 @@ def _invalid(msg):
 
 
 def _op_stream(stream, tensors):
-    """Raw stream of a call whose tensors must share one CUDA device (the
-    library takes addresses only): `stream`, or that device's current one."""
+    """Raw stream of a call whose tensors share the current CUDA device (the
+    library takes addresses only and launches there): `stream`, which must be
+    of that device too, or its current one."""
     dev = tensors[0].get_device()
     if dev < 0:
         _invalid("tensors must be on a CUDA device")
     for t in tensors:
         if t.get_device() != dev:
             _invalid("tensors must share one CUDA device")
-    return _current_raw_stream(dev) if stream is None else stream.cuda_stream
+    if dev != _current_device():
+        _invalid(f"tensors on cuda:{dev}, which is not the current device")
+    if stream is None:
+        return _current_raw_stream(dev)
+    if stream.device.index != dev:
+        _invalid(f"tensors on cuda:{dev}, stream on {stream.device}")
+    return stream.cuda_stream
 
 
 def _matrix(t, what):

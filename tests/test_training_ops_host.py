@@ -140,3 +140,24 @@ def test_distill_refuses_what_its_arithmetic_cannot_hold(lib, which):
     # log2(e) / T must be finite
     for T in (1e-45, 1e-39):
         assert dist(lib, which, T=T) == B.MO_ERR_INVALID_ARG, T
+
+
+class _On:
+    """What _op_stream asks of a tensor or a stream."""
+
+    def __init__(self, device, handle=0):
+        self.device, self.cuda_stream = torch.device("cuda", device), handle
+
+    def get_device(self):
+        return self.device.index
+
+
+def test_tensors_and_streams_of_another_device_are_refused(monkeypatch):
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    monkeypatch.setattr(B, "_current_raw_stream", lambda device: 100 + device)
+    assert B._op_stream(None, (_On(0), _On(0))) == 100
+    assert B._op_stream(_On(0, 7), (_On(0),)) == 7
+    for stream, tensors in ((None, (_On(1), _On(1))), (_On(1, 7), (_On(1),)), (_On(1, 7), (_On(0),)), (None, (_On(0), _On(1)))):
+        with pytest.raises(B.MoError) as e:
+            B._op_stream(stream, tensors)
+        assert e.value.status == B.MO_ERR_INVALID_ARG
