@@ -314,8 +314,8 @@ int embedding_grad(const void* dY, int dy_dtype, int64_t n, int64_t dim, int64_t
  * also none); offsets is a DEVICE array of experts + 1 int32, non-decreasing,
  * within [0, rows] (other values give wrong results, never an access out of
  * range).  W holds one n x k matrix for each expert, expert e at
- * W + e * stride_w (elements), ldw >= k.  bf16 operands on the tensor cores,
- * float32 sums:
+ * W + e * stride_w (elements), ldw >= k, stride_w >= n * ldw (unused with one
+ * expert).  bf16 operands on the tensor cores, float32 sums:
  *   expert_linear        Y[r, :]  = X[r, :] W_e^T                  (rows x n)
  *   expert_linear_dgrad  dX[r, :] = dY[r, :] W_e                   (rows x k)
  *   expert_linear_wgrad  dW_e (+)= sum_r dY[r, :]^T X[r, :]        (n x k each)

@@ -422,6 +422,12 @@ def _op_stream(stream, tensors):
     return stream.cuda_stream
 
 
+def _row_pitch(cols):
+    """The leading dimension given for a single row, on which nothing depends: any aligned
+    value, the same for every tensor of that row."""
+    return (cols + 7) // 8 * 8
+
+
 def _matrix(t, what):
     """(address, type code, rows, cols, ld) of a float32 or bf16 matrix."""
     if t.dim() != 2:
@@ -430,7 +436,7 @@ def _matrix(t, what):
     if cols > 1 and unit != 1:
         _invalid(f"{what} must have unit column stride")
     if rows <= 1:
-        ld = (max(ld, cols) + 7) // 8 * 8          # of a single row nothing depends on it: any aligned value
+        ld = _row_pitch(cols)
     code = _DTYPES.get(t.dtype)
     if code is None:
         _invalid(f"{what}: unsupported dtype {t.dtype}")
@@ -500,8 +506,8 @@ def _stack(t, what):
     if cols > 1 and unit != 1:
         _invalid(f"{what} must have unit column stride")
     if rows <= 1:
-        ld = (max(ld, cols) + 7) // 8 * 8
-    if experts <= 1:
+        ld = stride if rows == 1 and experts > 1 else _row_pitch(cols)   # (the stride's own checks hold for it)
+    if experts <= 1 or rows == 0:
         stride = rows * ld
     code = _DTYPES.get(t.dtype)
     if code is None:

@@ -284,3 +284,36 @@ def test_large_sizes_against_float64_on_the_device():
                                       (dW[e], d.T @ x, d.abs().T @ x.abs(), max(b - a, 1))):
             tol = (depth + 2) * 2.0 ** -23 * mag + 2.0 ** -24 * want.abs()
             assert bool(((got.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("k", [12, 8, 100])
+@pytest.mark.parametrize("permuted", [False, True])
+def test_stacks_of_one_row_matrices(k, permuted):
+    """Several experts of one output feature each: a matrix of one row needs no pitch of its own, only
+    a stack stride of whole 16 bytes."""
+    rng = np.random.default_rng(k)
+    off = _offsets([20, 0, 31])
+    dY, X = _mat(rng, 51, 1), _mat(rng, 51, k)
+    buf = torch.full((3, 1, _pad8(k)) if not permuted else (1, 3, _pad8(k)), 3.0, device=dev())
+    if k == 12 and not permuted:
+        buf = torch.full((3, 1, 12), 3.0, device=dev())                 # 48 bytes
+    dW = (buf.transpose(0, 1) if permuted else buf)[:, :, :k]
+    o, ws = torch.from_numpy(off).to(dev()), _ws(51, 1, k, 3)
+    mo.expert_linear_wgrad(dY, X, o, dW, ws)
+    x, dy = _f64(X), _f64(dY)
+    _assert_close(dW, ot.expert_linear_wgrad(dy, x, off), ot.expert_linear_wgrad(np.abs(dy), np.abs(x), off), 31)
+    W = torch.from_numpy(rng.standard_normal((1, 3, _pad8(k)))).to(BF16).to(dev()).transpose(0, 1)[:, :, :k]
+    Y = torch.empty((51, 8), device=dev())[:, :1]
+    mo.expert_linear(X, W, o, Y, ws)
+    w = _f64(W)
+    _assert_close(Y, ot.expert_linear(x, w, off), ot.expert_linear(np.abs(x), np.abs(w), off), k)
+    assert mo.mo_check_device_status(ws) == 0
+
+
+def test_a_product_over_no_features_is_zero():
+    """n == 0: the input's gradient is an empty sum, whatever the empty stack's strides."""
+    dX = torch.full((5, 16), 3.0, device=dev())[:, :13]
+    o, ws = torch.tensor([0, 2, 5], dtype=torch.int32, device=dev()), _ws(5, 0, 13, 2)
+    mo.expert_linear_dgrad(torch.empty((5, 0), dtype=BF16, device=dev()), torch.empty((2, 0, 13), dtype=BF16, device=dev()),
+                           o, dX, ws)
+    assert torch.all(dX == 0)

@@ -161,3 +161,15 @@ def test_tensors_and_streams_of_another_device_are_refused(monkeypatch):
         with pytest.raises(B.MoError) as e:
             B._op_stream(stream, tensors)
         assert e.value.status == B.MO_ERR_INVALID_ARG
+
+
+def test_pitches_of_single_rows_do_not_depend_on_their_strides():
+    t = torch.zeros((3, 2, 100))
+    assert B._matrix(t[:, 0][:1], "") == B._matrix(t[0, 0][None], "")          # the same row
+    for dtype, k in ((torch.float32, 12), (torch.bfloat16, 24)):
+        for stack in (torch.zeros((2, 1, k), dtype=dtype), torch.zeros((1, 2, k), dtype=dtype).transpose(0, 1)):
+            *_, experts, rows, cols, ld, stride = B._stack(stack, "")
+            assert (experts, rows, cols, stride) == (2, 1, k, k) and cols <= ld and rows * ld <= stride
+            assert ld * stack.element_size() % 16 == 0
+    *_, ld, stride = B._stack(torch.zeros((1, 1, 13)), "")
+    assert ld >= 13 and ld % 4 == 0 and stride % 4 == 0
