@@ -283,7 +283,9 @@ int plan_owners(const int64_t* rows, const int64_t* cols, int n, int world, int 
  * gradients that muon_step_batched and the AdamW tail consume.  Matrices are
  * row-major with a leading dimension in elements, as above; element
  * alignment suffices unless an entry says otherwise.  Outputs must not overlap
- * inputs unless an entry says so.  All sums are float32.
+ * inputs unless an entry says so.  All sums are float32; those on the tensor
+ * cores (expert_linear*) truncate within pieces of 768 terms (float32 results)
+ * or 4096 terms (bf16 results), whose sums are added rounded to nearest.
  * ------------------------------------------------------------------------ */
 
 /* Embedding lookup: out[i, :] = scale * W[ids[i], :] for i < n, W vocab x dim

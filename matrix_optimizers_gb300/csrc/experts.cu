@@ -966,6 +966,12 @@ std::atomic<int> g_expert_shape{-1};
 // never 2.1e-6 / 7.6e-5.  Shorter pieces hold the MMAs up while the epilogue stores:
 // 16384 rows, 8 experts of 4096 x 4096: 10 blocks 368 us, 12 blocks 340 us, 16 blocks 327 us.
 constexpr int kF32Chunk = 12;
+// A bf16 result's sums leave it every kBf16Chunk K blocks (4096 terms), which lose at most
+// 256 x 2^-23, a hundredth of the result's own rounding.  Left there, the drift grows with the length:
+// 2^20 positive terms came out 6.6e-3 too small on average, now 1.4e-5.  Pieces that long cost
+// nothing that shows (16384 rows, 8 experts of 4096 x 11008, forward and dgrad 816 and 851 us before, 822 and 860 now
+// in a run whose repeats differ by 20; 65536 rows of one 2048 x 2560 378 and 389, now 377 and 395).
+constexpr int kBf16Chunk = 64;
 
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 512;
 constexpr int64_t kMaxSide = int64_t(1) << 20;
@@ -1125,7 +1131,7 @@ int run_expert(int mode, const Request& q, void* ws, size_t ws_bytes, mo_stream_
     p.k = static_cast<int32_t>(q.k);
     p.experts = q.experts;
     p.splits = plan.splits;
-    p.chunk = f32 ? kF32Chunk : 1 << 26;                 // more blocks than any sum has
+    p.chunk = f32 ? kF32Chunk : kBf16Chunk;
     p.err = static_cast<int*>(ws);
     return op_status(op_traced(MO_K_EXPERT + mode, s, [&] {
         const bool acc = !split && q.accumulate;        // (split: the join adds)

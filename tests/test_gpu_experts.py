@@ -317,3 +317,48 @@ def test_a_product_over_no_features_is_zero():
     mo.expert_linear_dgrad(torch.empty((5, 0), dtype=BF16, device=dev()), torch.empty((2, 0, 13), dtype=BF16, device=dev()),
                            o, dX, ws)
     assert torch.all(dX == 0)
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("mode", ["forward", "dgrad", "wgrad"])
+def test_long_bf16_sums_do_not_drift(mode, geometry):
+    """The tensor core's accumulator drops bits always towards zero: each 16-term step may
+    lose 2^-23 of a sum of positive terms.  Over at most 4096 terms that is 256 x 2^-23, and
+    the float32 additions of the pieces (depth / 4096 of them) lose at most 2^-24 each; both
+    together bound the mean relative error.  The bf16 roundings, each up to 2^-8 and uniform
+    over the results' spread, average out to 2^-8 / sqrt(3 count); five times that is allowed.
+    Rows and columns are so many that no geometry splits the sums."""
+    g = torch.Generator(device=dev()).manual_seed(3)
+    depth, rows, cols, some = 1 << 20, 1024, 2560, 16
+    # factors that spread the results evenly over a binade
+    fr = torch.exp2(torch.linspace(0, 1, rows + 1, device=dev())[:rows])
+    fc = torch.exp2(torch.linspace(0, 1, cols + 1, device=dev())[:cols])
+
+    def pos(f, *shape):
+        return torch.rand(shape, generator=g, device=dev()).add_(0.5).mul_(f).to(BF16)
+
+    if mode == "wgrad":                                # dW [rows, cols] = dY^T X
+        a, b = pos(fr, depth, rows), pos(fc, depth, cols)
+        o, ws = torch.tensor([0, depth], dtype=torch.int32, device=dev()), _ws(depth, rows, cols, 1)
+        out = torch.empty((1, rows, cols), dtype=BF16, device=dev())
+        mo.expert_linear_wgrad(a, b, o, out, ws)
+        got, terms = out[0, :some], lambda i, j: (a[i:j, :some].double(), b[i:j].double())
+    else:                                              # cols tokens, rows features: out [cols, rows]
+        a, o = pos(fc[:, None], cols, depth), torch.tensor([0, cols], dtype=torch.int32, device=dev())
+        out = torch.empty((cols, rows), dtype=BF16, device=dev())
+        if mode == "forward":
+            w, ws = pos(fr[:, None], 1, rows, depth), _ws(cols, rows, depth, 1)
+            mo.expert_linear(a, w, o, out, ws)
+            terms = lambda i, j: (w[0, :some, i:j].double().T, a[:, i:j].double().T)
+        else:
+            w, ws = pos(fr, 1, depth, rows), _ws(cols, depth, rows, 1)
+            mo.expert_linear_dgrad(a, w, o, out, ws)
+            terms = lambda i, j: (w[0, i:j, :some].double(), a[:, i:j].double().T)
+        got = out[:, :some].T
+    want = torch.zeros((some, cols), dtype=torch.float64, device=dev())
+    for i in range(0, depth, 1 << 16):
+        l, r = terms(i, i + (1 << 16))
+        want += l.T @ r
+    assert mo.mo_check_device_status(ws) == 0
+    drift = float(((got.double() - want) / want).mean().abs())
+    assert drift <= 256 * 2.0 ** -23 + depth / 4096 * 2.0 ** -24 + 5 * 2.0 ** -8 / (3 * some * cols) ** 0.5, drift
