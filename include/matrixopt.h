@@ -359,7 +359,8 @@ int expert_linear_wgrad(const void* dY, int64_t ldy, const void* X, int64_t ldx,
  * elsewhere propagates within its row.
  *   distill_topk_loss       writes loss[n] and stats[n][2] = {max s, sum exp((s - max)/T)}
  *   distill_topk_grad       from the same inputs and stats writes dlogits
- *   distill_topk_loss_grad  both in one pass over the logits
+ *   distill_topk_loss_grad  both in one call: the second read of the logits
+ *                           finds most of them in L2
  * dlogits is n x vocab, float32 or bf16, ldg >= vocab; it may be the logits
  * themselves (same type and ld).  1 <= top <= 1024 (MO_ERR_UNSUPPORTED
  * above), vocab < 2^31 - 1024, T a normal float32.  n == 0 is a no-op. */

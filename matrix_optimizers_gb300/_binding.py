@@ -615,7 +615,8 @@ def distill_topk_grad(logits, idx, teacher, stats, dlogits, temperature=1.0, row
 
 def distill_topk_loss_grad(logits, idx, teacher, loss, dlogits, temperature=1.0, row_weight=None, grad_scale=1.0,
                            stream=None):
-    """Loss and gradient in one pass over the logits; dlogits may be the logits."""
+    """Loss and gradient in one call, which reads the logits a second time mostly from L2;
+    dlogits may be the logits."""
     s = _op_stream(stream, (logits, idx, teacher, loss, dlogits) + (() if row_weight is None else (row_weight,)))
     d = _distill(logits, idx, teacher, temperature, row_weight, grad_scale)
     g, code, ld = _dlogits(dlogits, logits)

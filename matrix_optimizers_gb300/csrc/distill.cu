@@ -36,7 +36,10 @@ constexpr int64_t kMaxVocab = INT32_MAX - 1024;       // a thread's next column,
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
 constexpr int kRowAhead = 4;                          // 16-byte pieces in flight per thread
 constexpr int kMaxCluster = 8;
-constexpr int64_t kSliceBytes = 65536;                // of a row, per CTA, when loss and gradient are wanted
+// of a row, per CTA, when loss and gradient are wanted.  Rows past eight such slices get larger ones and
+// are read again from DRAM in part (2048 float32 rows: 131072 logits 355 us, 6.0 TB/s of their two passes; 200064
+// logits 714 us, 4.6 TB/s, and 732 as two calls).
+constexpr int64_t kSliceBytes = 65536;
 
 struct DistillArgs {
     mo_distill d;
@@ -275,7 +278,9 @@ __device__ __forceinline__ float row_loss(const DistillArgs& a, const Teacher& t
 
 // The gradient at the teacher's places for which mine(place) holds, after the
 // block has written the rest.  A place that several entries name is written once,
-// by the first of them.
+// by the first of them.  Every entry is compared with every other, which is nothing for the
+// few entries a teacher keeps and most of the time for many (2048 rows of 32000 bf16, loss and gradient:
+// 64 entries 56 us, 256 84, 1024 636).
 template <typename G, typename F>
 __device__ __forceinline__ void fix_places(const DistillArgs& a, const Teacher& t, const MaxSum& st, float coef, float inv,
                                            G* g, F&& mine) {
