@@ -352,8 +352,8 @@ int expert_linear_wgrad(const void* dY, int64_t ldy, const void* X, int64_t ldx,
  *   loss  = w T^2 sum_k p_k (log p_k - log q[idx_k])
  *   d s_j = g w T (q_j - sum of p_k over the k with idx_k == j)
  * where w = row_weight[row] (null: 1) and g = grad_scale.  T^2 keeps the
- * gradient's size independent of T.  Entries with p_k = 0 (t = -inf) add
- * nothing; q of a logit at -inf is 0 (a row of -inf only has q = 0 throughout),
+ * gradient's size independent of T.  Entries with p_k = 0 in float32 (t = -inf,
+ * or far enough below the others) add nothing; q of a logit at -inf is 0 (a row of -inf only has q = 0 throughout),
  * and p_k > 0 there makes the loss +inf.  A row with w = 0, or without a present
  * entry above -inf, has loss 0 and gradient 0 whatever its logits hold; NaN
  * elsewhere propagates within its row.
