@@ -476,7 +476,8 @@ int expert_combine_grad(const void* dY, int dy_dtype, int64_t ldy, const void* Y
  * block_norm_grad_workspace_bytes (host only; `gates` = rows of gate, 0 without
  * one; the same on every call with these sizes), no initialisation.
  * dim <= 8192, n < 2^31 (MO_ERR_UNSUPPORTED above); n == 0 or dim == 0: no rows,
- * parameter gradients are 0 (unchanged with accumulate = 1). */
+ * dpost and dpre are 0 (unchanged with accumulate = 1).  gate has no rows with
+ * n == 0, so that dgate is not written there: a caller who keeps some clears them. */
 typedef struct {
     int64_t n, dim, ldx, ldr, rows_per_gate, ldgate;
     int32_t x_dtype, stream_dtype, param_dtype;

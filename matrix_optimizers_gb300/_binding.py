@@ -877,7 +877,8 @@ def block_norm_grad(x, y, dy, dh, dx, ws, dresidual=None, post=None, gate=None, 
                     stream=None):
     """block_norm's gradients from x, the y it wrote (None without pre), dy (or None) and dh
     (None without pre): dx, dresidual (or None; may be dy), and the float32 gradients of the
-    parameters (each may be None; accumulate=True adds to them)."""
+    parameters (each may be None; accumulate=True adds to them).  Without rows these are 0, dgate
+    with all rows that it has."""
     s = _op_stream(stream, (x, dx, ws, y, dy, dh, dresidual, post, gate, pre, dpost, dgate, dpre))
     p, shape, code, gates = _norm_args(x, post, gate, pre, eps, residual_scale, block_scale, rows_per_gate)
     y_p, ldy, stream_code = _like(y, shape, "y", None)
@@ -895,6 +896,13 @@ def block_norm_grad(x, y, dy, dh, dx, ws, dresidual=None, post=None, gate=None, 
         None if dgate is None else _dense(dgate, _F32, each, "dgate"),
         None if dpre is None else _dense(dpre, _F32, vector, "dpre"), 1 if accumulate else 0, ws.data_ptr(), _nbytes(ws),
         s))
+    if shape[0] == 0 and dgate is not None and not accumulate:
+        # the library takes a gate's rows from x's (none here), a tensor has its own
+        if stream is None:
+            dgate.zero_()
+        else:
+            with torch.cuda.stream(stream):
+                dgate.zero_()
 
 
 ADAMW_BLOCK = 256      # values of one scale of the 8-bit states

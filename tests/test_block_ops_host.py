@@ -264,3 +264,21 @@ def test_adamw_list_refuses_tensors_that_overlap(on_cuda):
     B.adamw_tensors([B.make_adamw_tensor(W, g, m, v), B.make_adamw_tensor(z(512), g, z(512), z(512))])   # a gradient may be shared
     for kw in (dict(step=z(1)), dict(step=z(2, dtype=torch.int64)), dict(step=1, grad_mul=z(2))):
         refused(lambda: B.adamw_step_batched([a], **kw))
+
+
+@pytest.fixture
+def no_launch(monkeypatch, on_cuda):
+    """Calls end where the library's would begin, with success; their arguments are kept."""
+    made = []
+    monkeypatch.setattr(B, "_call", lambda name: lambda *a: made.append((name, a)) or B.MO_OK)
+    return on_cuda, made
+
+
+@pytest.mark.parametrize("gate_shape,rows_per_gate", [((8,), None), ((1, 8), None), ((8,), 4), ((3, 8), 4), ((0, 8), 4)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_without_rows_the_gradient_of_a_gate_is_zero(no_launch, gate_shape, rows_per_gate, accumulate):
+    z, made = no_launch
+    x, gate, dgate = z(0, 8), z(*gate_shape), z(*gate_shape) + 3
+    B.block_norm_grad(x, x, x, None, z(0, 8), z(256, dtype=torch.uint8), gate=gate, dgate=dgate, rows_per_gate=rows_per_gate,
+                      accumulate=accumulate)
+    assert len(made) == 1 and bool((dgate == (3 if accumulate else 0)).all())
