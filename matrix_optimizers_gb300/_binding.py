@@ -826,9 +826,9 @@ def _norm_args(x, post, gate, pre, eps, residual_scale, block_scale, rows_per_ga
             if cols != dim:
                 _invalid("gate must have rows of x's length")
         if rows_per_gate is None:
-            if gates == 0 or n % gates:
+            if n > 0 and (gates == 0 or n % gates):
                 _invalid("rows_per_gate is needed where the gate's rows do not divide x's")
-            rows_per_gate = n // gates or 1
+            rows_per_gate = n // gates if n > 0 else 1
         if rows_per_gate < 1 or (n > 0 and gates != -(-n // rows_per_gate)):
             _invalid("gate must be ceil(rows / rows_per_gate) x dim")
     values = [n, dim, ldx, 0, rows_per_gate or 1, ldgate, code, MO_F32, _DTYPES.get(dtype, MO_F32), eps, residual_scale,

@@ -282,3 +282,14 @@ def test_without_rows_the_gradient_of_a_gate_is_zero(no_launch, gate_shape, rows
     B.block_norm_grad(x, x, x, None, z(0, 8), z(256, dtype=torch.uint8), gate=gate, dgate=dgate, rows_per_gate=rows_per_gate,
                       accumulate=accumulate)
     assert len(made) == 1 and bool((dgate == (3 if accumulate else 0)).all())
+
+
+def test_an_empty_batch_may_have_a_gate_of_no_rows(no_launch):
+    """One gate for each sequence, and no sequences."""
+    z, made = no_launch
+    x, gate = z(0, 8), z(0, 8)
+    B.block_norm(x, x, None, gate=gate)
+    B.block_norm_grad(x, x, x, None, z(0, 8), z(256, dtype=torch.uint8), gate=gate, dgate=z(0, 8))
+    assert [name for name, _ in made] == ["block_norm", "block_norm_grad"]
+    refused(lambda: B.block_norm(z(4, 8), z(4, 8), None, gate=gate))
+    assert len(made) == 2
