@@ -517,7 +517,8 @@ int block_norm_grad(const mo_block_norm* p, const void* y, int64_t ldy, const vo
  * in the list, index in the tensor modulo 2^32): the same inputs give the same bits.
  * The step number (>= 1) is `step`, or, with step_ptr not null, the device int64
  * there, which a captured graph reads on each replay.
- * The tensors must not overlap.  numel == 0 is skipped, numel < 2^40
+ * What is written must not overlap, nor a gradient overlap it (gradients may each
+ * other).  numel == 0 is skipped, numel < 2^40
  * (MO_ERR_UNSUPPORTED above); beta1, beta2 in [0, 1), eps >= 0. */
 typedef struct {
     int64_t     numel;

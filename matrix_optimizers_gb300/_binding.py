@@ -938,11 +938,20 @@ def make_adamw_tensor(W, g, m, v, m_scale=None, v_scale=None, lr=1e-3, weight_de
     return t
 
 
-def _check_apart(tensors):
-    """Refuses contiguous tensors that overlap."""
-    spans = sorted((t.data_ptr(), t.nbytes) for t in tensors if t.nbytes)
-    if any(a + size > b for (a, size), (b, _) in zip(spans, spans[1:])):
-        _invalid("the tensors that are written must not overlap (is one of them in the list twice?)")
+def _check_apart(written, read):
+    """Refuses contiguous tensors that are written and overlap, with each other or with one that is read."""
+    spans = [(t.data_ptr(), t.nbytes, True) for t in written] + [(t.data_ptr(), t.nbytes, False) for t in read]
+    spans.sort()
+    end_written = end = 0                          # of the spans so far: those written, all
+    for at, size, writes in spans:
+        if size == 0:
+            continue
+        if at < (end if writes else end_written):
+            _invalid("the tensors that are written must not overlap, nor a gradient overlap one (is a tensor in the "
+                     "list twice?)")
+        end = max(end, at + size)
+        if writes:
+            end_written = at + size
 
 
 class adamw_tensors:
@@ -956,7 +965,7 @@ class adamw_tensors:
         for t in self.tensors:
             if t.get_device() < 0 or t.get_device() != self.tensors[0].get_device():
                 _invalid("tensors must share one CUDA device")
-        _check_apart([t for d in tensors for t in d.tensors[:1] + d.tensors[2:]])
+        _check_apart([t for d in tensors for t in d.tensors[:1] + d.tensors[2:]], [d.tensors[1] for d in tensors])
 
 
 def adamw_step_batched(tensors, step, beta1=0.9, beta2=0.95, eps=1e-8, grad_scale=1.0, grad_mul=None, seed=None,

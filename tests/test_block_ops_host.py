@@ -293,3 +293,26 @@ def test_an_empty_batch_may_have_a_gate_of_no_rows(no_launch):
     assert [name for name, _ in made] == ["block_norm", "block_norm_grad"]
     refused(lambda: B.block_norm(z(4, 8), z(4, 8), None, gate=gate))
     assert len(made) == 2
+
+
+def test_adamw_list_refuses_a_gradient_that_another_tensor_s_step_writes(on_cuda):
+    z = on_cuda
+    mine = lambda: [z(512) for _ in range(4)]  # noqa: E731
+    (W, g, m, v), (W2, g2, m2, v2) = mine(), mine()
+    make = B.make_adamw_tensor
+    for k in (W, m, v):
+        refused(lambda: B.adamw_tensors([make(W, g, m, v), make(W2, k, m2, v2)]))
+        refused(lambda: B.adamw_tensors([make(W2, k, m2, v2), make(W, g, m, v)]))
+    refused(lambda: B.adamw_tensors([make(W, W, m, v)]))
+    whole = z(2000)
+    for at in (0, 1, 511, 1000, 1022):                   # of the gradient's 512; W has 511 .. 1022
+        t = [make(whole[511:1023], g, m, v), make(W2, whole[at: at + 512], m2, v2)]
+        refused(lambda: B.adamw_tensors(t)) if at else B.adamw_tensors([make(whole[512:1024], g, m, v), t[1]])
+    B.adamw_tensors([make(whole[511:1023], g, m, v), make(W2, whole[1023:1535], m2, v2)])
+    s = z(4)
+    e, f = (z(512, dtype=torch.float8_e4m3fn) for _ in range(2))
+    refused(lambda: B.adamw_tensors([make(W, g, e, f, s[:2], s[2:]), make(z(2), s[1:3], z(2), z(2))]))
+    # gradients that share memory among themselves, a long one over short ones
+    B.adamw_tensors([make(W, whole[:512], m, v), make(W2, whole[100:612], m2, v2), make(z(2000), whole, z(2000), z(2000))])
+    refused(lambda: B.adamw_tensors([make(z(2000), whole, z(2000), z(2000)), make(W, whole[:5].new_zeros(512), m, v),
+                                     make(whole[1990:], z(10), z(10), z(10))]))
