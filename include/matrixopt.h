@@ -519,7 +519,7 @@ int block_norm_grad(const mo_block_norm* p, const void* y, int64_t ldy, const vo
  * there, which a captured graph reads on each replay.
  * What is written must not overlap, nor a gradient overlap it (gradients may each
  * other).  numel == 0 is skipped, numel < 2^40
- * (MO_ERR_UNSUPPORTED above); beta1, beta2 in [0, 1), eps >= 0. */
+ * (MO_ERR_UNSUPPORTED above); beta1, beta2 in [0, 1), eps in [0, 2^125]. */
 typedef struct {
     int64_t     numel;
     void*       W;

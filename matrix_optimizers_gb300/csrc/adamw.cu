@@ -231,7 +231,7 @@ __device__ __forceinline__ void step_values(const Desc& d, const Step& c, int64_
         v[i] = __fadd_rn(__fmul_rn(c.beta2, v[i]), __fmul_rn(c.one_minus2, __fmul_rn(gi, gi)));
         root[i] = __fsqrt_rn(v[i]);
         const float denom = fmaf(root[i], c.root_inv_bc2, c.eps);
-        w[i] = w[i] - c.decay * w[i] - c.lr * __fdividef(m[i], denom);                 // (denom < 2^126: within 2 u)
+        w[i] = w[i] - c.decay * w[i] - c.lr * __fdividef(m[i], denom);                 // (denom below 2^126, or infinite with v: within 2 u)
     }
     store8<kFull>(d.W, d.w_dtype, at, valid, w);
     if (kCodes) {
@@ -325,6 +325,9 @@ cudaError_t launch_batch(const Common& common, const Desc* d, int count, int64_t
 
 constexpr int kFew = 8, kSome = 64, kMany = 320;   // descriptors of a launch; 320 fill the 32 KB of parameters
 constexpr int64_t kMaxNumel = int64_t(1) << 40;
+// The update divides by __fdividef, which gives 0 for a divisor above 2^126.  sqrt(v / (1 - beta2^t)) is below 2^76
+// (v below 2^128, 1 - beta2 at least 2^-24), so that with such an eps the divisor stays below 2^126.
+constexpr float kMaxEps = 0x1p125f;
 
 int check_tensor(const mo_adamw_tensor& t) {
     const bool small = t.state_dtype == MO_E4M3;
@@ -351,7 +354,8 @@ using namespace mo;
 extern "C" int adamw_step_batched(const mo_adamw_tensor* tensors, int count, const mo_adamw_cfg* cfg,
                                   mo_stream_t stream) {
     if (count < 0 || cfg == nullptr || (count > 0 && tensors == nullptr) || (cfg->dither != 0 && cfg->dither != 1) ||
-        !(cfg->beta1 >= 0.f && cfg->beta1 < 1.f) || !(cfg->beta2 >= 0.f && cfg->beta2 < 1.f) || !(cfg->eps >= 0.f) ||
+        !(cfg->beta1 >= 0.f && cfg->beta1 < 1.f) || !(cfg->beta2 >= 0.f && cfg->beta2 < 1.f) ||
+        !(cfg->eps >= 0.f && cfg->eps <= kMaxEps) ||
         (cfg->step_ptr == nullptr && cfg->step < 1))
         return MO_ERR_INVALID_ARG;
     if (!op_aligned(cfg->step_ptr, 8) || !op_aligned(cfg->grad_mul, 4)) return MO_ERR_ALIGNMENT;

@@ -316,3 +316,9 @@ def test_adamw_list_refuses_a_gradient_that_another_tensor_s_step_writes(on_cuda
     B.adamw_tensors([make(W, whole[:512], m, v), make(W2, whole[100:612], m2, v2), make(z(2000), whole, z(2000), z(2000))])
     refused(lambda: B.adamw_tensors([make(z(2000), whole, z(2000), z(2000)), make(W, whole[:5].new_zeros(512), m, v),
                                      make(whole[1990:], z(10), z(10), z(10))]))
+
+
+def test_adamw_batch_refuses_an_eps_beyond_its_division(lib):
+    for eps in (2.0 ** 125 * 1.0001, 2e38, float("inf"), float("nan")):
+        assert adam(lib, cfg=dict(eps=eps)) == INV, eps
+    assert adam(lib, cfg=dict(eps=2.0 ** 125), numel=0, W=None, g=None, m=None, v=None) == B.MO_OK

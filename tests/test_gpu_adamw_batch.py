@@ -188,3 +188,18 @@ def test_a_list_and_another_stream_give_the_same():
     mo.adamw_step_batched(mo.adamw_tensors([b.make()]), 4, seed=1, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(a.W, b.W) and torch.equal(a.m.view(torch.uint8), b.m.view(torch.uint8))
+
+
+@pytest.mark.parametrize("w", [F32, BF16])
+@pytest.mark.parametrize("eps", [1e-30, 1e-38, 1e-40, 1e-44, 1e32, 2.0 ** 125])
+def test_an_eps_of_any_size(eps, w):
+    """Gradients of 1e-25 leave float32 roots of v of 0, so that eps alone divides their m of 1e-26; beside
+    them gradients that hide the smallest eps, and with the largest the moves are small ones."""
+    for state in (F32, E4M3):
+        p = Param(np.random.default_rng(6), 3 * 256, w=w, state=state, lr=1e-10 if eps < 1 else 1e32, decay=0.0, zero=True)
+        g = 0.01 * np.random.default_rng(7).standard_normal(3 * 256).astype(np.float32)
+        g[:256] *= 1e-23
+        p.g.copy_(torch.from_numpy(g))
+        before = p.copy()
+        mo.adamw_step_batched([p.make()], 3, eps=eps)
+        _check(p, before, 0, 3, eps=eps)
