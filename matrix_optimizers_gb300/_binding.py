@@ -956,7 +956,8 @@ def _check_apart(written, read):
 
 class adamw_tensors:
     """A list of make_adamw_tensor results laid out once, for adamw_step_batched; it keeps
-    their tensors alive."""
+    their tensors alive.  `array` holds the descriptors, which every call reads anew: a rate that changes
+    is written to array[i].lr (or .weight_decay) between steps.  A captured step keeps those of its capture."""
 
     def __init__(self, tensors):
         self.count = len(tensors)

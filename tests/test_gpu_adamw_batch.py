@@ -203,3 +203,17 @@ def test_an_eps_of_any_size(eps, w):
         before = p.copy()
         mo.adamw_step_batched([p.make()], 3, eps=eps)
         _check(p, before, 0, 3, eps=eps)
+
+
+def test_a_rate_and_a_decay_changed_in_the_list_count_from_the_next_step():
+    rng = np.random.default_rng(9)
+    ps = [Param(rng, 700, state=s) for s in (F32, E4M3)]
+    tensors = mo.adamw_tensors([p.make() for p in ps])
+    for step, (lr, decay) in enumerate(((1e-3, 0.1), (4e-3, 0.0), (0.0, 0.2)), 1):
+        for i, p in enumerate(ps):
+            p.lr, p.decay = lr, decay
+            tensors.array[i].lr, tensors.array[i].weight_decay = lr, decay
+        before = [p.copy() for p in ps]
+        mo.adamw_step_batched(tensors, step)
+        for i, p in enumerate(ps):
+            _check(p, before[i], i, step)
