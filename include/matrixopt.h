@@ -505,10 +505,10 @@ int block_norm_grad(const mo_block_norm* p, const void* y, int64_t ldy, const vo
  *   m = m_scale q,  v = (v_scale s)^2       with q and s e4m3 values in m and v
  * and ceil(numel / 256) float32 scales of each; zeros throughout are the zero
  * state.  Then the update of W uses the new m and v in float32, before they are
- * rounded: with a = max |m| over the block, m_scale = a / 448 and
+ * rounded: with a = max |m| over the block, m_scale = a (1 / 448) and
  *   q = round((m (1 / a)) 448),   s = the same of sqrt(v), a positive one at least 2^-9
- * each operation one float32 rounding to nearest (beta m + (1 - beta) g without
- * fused products), so that the states are reproducible bit for bit.  A block with a
+ * each operation one float32 rounding to nearest (1 / 448, too; beta m + (1 - beta) g
+ * without fused products), so that the states are reproducible bit for bit.  A block with a
  * < 2^-126 is stored as 0; one with a value that is not finite as NaN throughout.
  * dither = 0 rounds to the nearest e4m3 value, ties to even.  A decay by less than
  * half a step (1/32 to 1/16 of a value) is lost then; dither = 1 rounds at random
@@ -517,8 +517,8 @@ int block_norm_grad(const mo_block_norm* p, const void* y, int64_t ldy, const vo
  * in the list, index in the tensor modulo 2^32): the same inputs give the same bits.
  * The step number (>= 1) is `step`, or, with step_ptr not null, the device int64
  * there, which a captured graph reads on each replay.
- * What is written must not overlap, nor a gradient overlap it (gradients may each
- * other).  numel == 0 is skipped, numel < 2^40
+ * What is written must not overlap, nor a gradient overlap it; gradients may overlap
+ * each other.  numel == 0 is skipped, numel < 2^40
  * (MO_ERR_UNSUPPORTED above); beta1, beta2 in [0, 1), eps in [0, 2^125]. */
 typedef struct {
     int64_t     numel;

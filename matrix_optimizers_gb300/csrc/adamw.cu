@@ -6,7 +6,7 @@
 // tensor by bisection.  A warp takes 256 neighbouring values at a time, eight to a
 // lane: one block of the 8-bit states, whose largest value is a maximum over the warp.
 //
-// Float32 states are bound by their bytes (14 to 28 a value).  8-bit ones are near the
+// Float32 states are bound by their bytes (22 to 28 a value with bf16 or float32 weights and gradients).  8-bit ones are near the
 // point where instructions count as much: 16 bytes a value allow about 90.
 #include <cmath>
 

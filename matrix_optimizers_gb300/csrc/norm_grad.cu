@@ -280,7 +280,8 @@ cudaError_t launch_grad(GradArgs& a, cudaStream_t s) {
 // Rows of 67 million values, bf16 with a float32 stream, in us: 1024 columns 191, 211, 246; 2048 191, 211,
 // 255; 3000 227, 199, 326; 4096 214, 192, 237; 5120 -, 196, 287.  All bf16 (pieces of eight, few spills):
 // 512 columns 149, 151, 154; 1024 155, 137, 147; 2048 163, 141, 153; and 4096, where 512 threads have two
-// rows and 384 only one, 190, 169, 155.
+// rows and 384 only one, 190, 169, 155.  These rows lie on 16-byte boundaries; off them the all-bf16 rule holds,
+// too: 4001 columns -, 310, 292; 3500 -, 345, 343.
 template <typename X, typename S, typename F>
 cudaError_t with_columns(int64_t dim, F&& f) {
     constexpr bool kSmall = sizeof(X) + sizeof(S) == 4;

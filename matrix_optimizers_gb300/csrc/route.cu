@@ -276,7 +276,7 @@ __device__ __forceinline__ float bound_of(float v, int top, int sub, int group) 
 // The same as choose_in_rounds for up to G choices without rounds over all logits: the top-th largest of the
 // lanes' maxima is a bound that at least `top` logits reach and few others do (8 choices of 16 lanes: 10.6 on
 // average if the logits are in random order); those that reach it are gathered, one to a lane, and each counts
-// the ones before it.  8 of 128 experts for 65536 rows: 36 us forward, 55 by rounds.
+// the ones before it.  8 of 128 experts for 65536 rows: 37 us forward, 55 by rounds.
 //
 // gather: `count` of them in `list`; false if a group has more than G, as with many equal logits, or fewer
 // than `top` lanes that hold anything.
@@ -335,7 +335,7 @@ __device__ __forceinline__ void choose_from(uint64_t* list, int count, const Cho
 }
 
 // Blocks on an SM: as many as spill little (65536 float32 rows, 8 of 1024: 107 us with two, 157 with one, 159
-// with three; of 512 68 us with four, 77 with three; of 256 49 with four, 52 with five).
+// with three; of 512 68 us with four, 77 with three; of 256 48 with four, 52 with five, and the gradient 29 and 49).
 template <int V>
 constexpr int kRouteResident = V <= 16 ? 4 : 2;
 
@@ -778,9 +778,10 @@ struct RouteLayout {
     int rows, words, chunks;
 };
 
-// As many chunks as blocks fit on the device at once (four on each SM), of 32 to 128 rows, and
-// of no fewer than a block takes at a time (64 with up to 32 experts):
-// 65536 rows of 256 in 586 chunks of 112 take 45 us, in 512 of 128 (three or four to an SM) 51 us.
+// As many chunks as blocks of up to 512 experts fit on a whole GB300 at once (four on each of 152 SMs; with more
+// experts two fit, and the chunks take two turns), of 32 to 128 rows, and of no fewer than a block takes at a time
+// (64 with up to 32 experts): 65536 rows of 256 in 586 chunks of 112 take 48 us, in 512 of 128 52 us; of 1024
+// 107 and 116 us.  A constant, as the workspace's size is asked for without a device.
 constexpr int64_t kMostChunks = 4 * 152;
 RouteLayout route_layout(int64_t n, int experts) {
     RouteLayout L;
@@ -804,7 +805,7 @@ RouteLayout route_layout(int64_t n, int experts) {
 }
 
 // (G, V) by the number of experts: eight rows to a warp up to 32 experts, two up to 128, else one.  Two
-// rows of 256 to a warp were as fast forward (46 us for 65536 rows) and slower back (38 us, 31 with one).
+// rows of 256 to a warp are slower (65536 rows: 52 us forward and 33 back, 48 and 29 with one).
 // warps: also up to 128 experts, for choices that half a warp seldom has gathered room for and that are few
 // among the experts (12 of 64 for 65536 rows 50 us, 64 with two rows to a warp; 16 of 128 52, 107; but 8 of 128
 // 41, 37, and 16 of 64 103, 78).
