@@ -6,6 +6,7 @@ torch tensors / Python values into the C structures and pointers, and raises
 every step runs in the library's CUDA kernels (or, for ``plan_owners``, in
 its host C++).  If the library has not been built the first call raises.
 """
+import bisect
 import ctypes
 import os
 import struct
@@ -940,18 +941,17 @@ def make_adamw_tensor(W, g, m, v, m_scale=None, v_scale=None, lr=1e-3, weight_de
 
 def _check_apart(written, read):
     """Refuses contiguous tensors that are written and overlap, with each other or with one that is read."""
-    spans = [(t.data_ptr(), t.nbytes, True) for t in written] + [(t.data_ptr(), t.nbytes, False) for t in read]
-    spans.sort()
-    end_written = end = 0                          # of the spans so far: those written, all
-    for at, size, writes in spans:
-        if size == 0:
-            continue
-        if at < (end if writes else end_written):
-            _invalid("the tensors that are written must not overlap, nor a gradient overlap one (is a tensor in the "
-                     "list twice?)")
-        end = max(end, at + size)
-        if writes:
-            end_written = at + size
+    spans = sorted([(t.data_ptr(), t.nbytes) for t in written])
+    begins, ends = [at for at, size in spans if size], [at + size for at, size in spans if size]
+    apart = all(map(int.__le__, ends, begins[1:]))
+    for t in read if apart else ():
+        at, size = t.data_ptr(), t.nbytes
+        k = bisect.bisect_right(begins, at)                    # the spans before k begin at or before t
+        if size and ((k > 0 and ends[k - 1] > at) or (k < len(begins) and begins[k] < at + size)):
+            apart = False
+    if not apart:
+        _invalid("the tensors that are written must overlap neither each other nor a gradient (is one of them in the "
+                 "list twice?)")
 
 
 class adamw_tensors:
@@ -963,9 +963,9 @@ class adamw_tensors:
         self.count = len(tensors)
         self.array = (mo_adamw_tensor * max(1, self.count))(*tensors)
         self.tensors = [t for d in tensors for t in d.tensors]
-        for t in self.tensors:
-            if t.get_device() < 0 or t.get_device() != self.tensors[0].get_device():
-                _invalid("tensors must share one CUDA device")
+        devices = {t.get_device() for t in self.tensors}
+        if len(devices) > 1 or min(devices, default=0) < 0:
+            _invalid("tensors must share one CUDA device")
         _check_apart([t for d in tensors for t in d.tensors[:1] + d.tensors[2:]], [d.tensors[1] for d in tensors])
 
 
